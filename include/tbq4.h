@@ -359,6 +359,161 @@ TBQ4_API tbq4_status tbq4_attn_prefill_chunk(const uint16_t *q, int n_new,
                                     size_t ws_bytes, uint16_t *out,
                                     void *stream);
 
+/*
+ * Speculative decoding with draft trees, three calls of one step: the new
+ * tokens' queries and keys are rotated by their positions and keys and
+ * values appended (tbq4_rope_append), the tree's nodes attend to the context
+ * and to their ancestors (tbq4_attn_tree), and the accepted path is kept
+ * (tbq4_tree_accept).  The pages name drafted tokens (trefon.com, "Kontekst
+ * 262K na jednej RTX 4090", section "Konfiguracja": up to 3 of them, in a
+ * row); trees, position rotation and acceptance have no counterpart there.
+ * The first and the last call serve ordinary decoding and prefill as well.
+ */
+typedef enum { TBQ4_F32 = 0, TBQ4_F16 = 1, TBQ4_BF16 = 2 } tbq4_dtype;
+
+/*
+ * Rotary embedding and quantise-append in one launch.  Token t of the call
+ * belongs to sequence seq_ids[t], goes to cache position slots[t] and is
+ * rotated by position positions[t].
+ *   rotation  theta_i = positions[t] * inv_freq[i], i < rot_dim / 2, in
+ *             binary64; c, s = cos, sin of theta_i rounded to binary32; the
+ *             pair (x1, x2) of a query or key head becomes
+ *               y1 = x1 c - x2 s,  y2 = x2 c + x1 s
+ *             with every product, difference and sum rounded to binary32.
+ *             Pairs are channels (i, i + rot_dim / 2), or (2i, 2i + 1) with
+ *             interleaved != 0; channels from rot_dim on pass unchanged.
+ *   caches    the rotated keys and the values, encoded as by
+ *             tbq4_quantize_append (from binary32: a key is not rounded to
+ *             the input's type between rotation and encoding).  Bytes are
+ *             defined bit for bit.
+ *   q_out     the rotated queries, rounded once (to nearest even) to the
+ *             input's type.
+ * Arguments:
+ *   q, k, v    device, rows of 128 of type `dtype` (tbq4_dtype), 16-byte
+ *              aligned: head h of token t starts at element t * token_stride
+ *              + h * head_stride.  Strides are in elements, >= 0 and
+ *              multiples of 16 bytes, so the three may be slices of one
+ *              projection's output.  q may be NULL with Hq = 0.
+ *   seq_ids    device, int32 [n_tokens], or NULL: token t belongs to sequence
+ *              t / (n_tokens / B) (n_tokens a multiple of B).  A negative id
+ *              marks padding: nothing of that token is read or written.
+ *   slots      device, int32 [n_tokens]; two tokens of one call must not name
+ *              one slot of one sequence (the block would hold a mix of both)
+ *   positions  device, int32 [n_tokens], or NULL: the slots
+ *   inv_freq   device, double [rot_dim / 2] (NULL with rot_dim = 0: no
+ *              rotation); any frequency scaling is the caller's
+ *   rot_dim    0 .. 128, a multiple of 8
+ *   k_cache,
+ *   v_cache    as tbq4_quantize_append (or pools and a block table, as
+ *              tbq4_quantize_append_paged); distinct
+ *   q_out      device, [n_tokens][Hq][128] of type `dtype`, 16-byte aligned;
+ *              may be q itself where q has those strides
+ * A token whose id is >= B, or whose slot or page lies outside the cache, has
+ * no row written into the caches and flags TBQ4_ERR_CAPACITY in the device
+ * status.
+ * Errors: TBQ4_ERR_NULL, TBQ4_ERR_ALIGN (pointers, strides), TBQ4_ERR_SHAPE
+ * (dtype, sizes, rot_dim, k_cache == v_cache), TBQ4_ERR_CAPACITY (capacity),
+ * TBQ4_ERR_LAUNCH.
+ */
+TBQ4_API tbq4_status tbq4_rope_append(const void *q, int64_t q_token_stride, int64_t q_head_stride,
+                                      const void *k, int64_t k_token_stride, int64_t k_head_stride,
+                                      const void *v, int64_t v_token_stride, int64_t v_head_stride,
+                                      int dtype, int n_tokens, int B, int Hq, int Hkv,
+                                      const int32_t *seq_ids, const int32_t *slots,
+                                      const int32_t *positions, const double *inv_freq, int rot_dim,
+                                      int interleaved, int64_t capacity, uint64_t sign_seed,
+                                      uint8_t *k_cache, uint8_t *v_cache, void *q_out, void *stream);
+TBQ4_API tbq4_status tbq4_rope_append_paged(
+    const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *k,
+    int64_t k_token_stride, int64_t k_head_stride, const void *v, int64_t v_token_stride,
+    int64_t v_head_stride, int dtype, int n_tokens, int B, int Hq, int Hkv, const int32_t *seq_ids,
+    const int32_t *slots, const int32_t *positions, const double *inv_freq, int rot_dim,
+    int interleaved, const int32_t *block_table, int max_pages, int page_size, int64_t n_pages,
+    uint64_t sign_seed, uint8_t *k_pool, uint8_t *v_pool, void *q_out, void *stream);
+
+/*
+ * Tree attention.  Sequence b holds ctx_lens[b] cached tokens and, in the
+ * slots ctx_lens[b] + j right behind them, its n_nodes[b] drafted nodes
+ * (appended before this call).  Node i attends to every cached token and to
+ * the nodes j < n_nodes[b] whose bit j is set in its mask, itself only if its
+ * own bit is; nothing is implied by the order of the nodes.  A node that sees
+ * nothing gives a zero row.  Rows of nodes i >= n_nodes[b] are left as they
+ * were.  One node per sequence is an ordinary decode step.
+ *   q          device, [B][T][Hq][128] of type q_dtype, 16-byte aligned
+ *   ctx_lens   device, int32 [B]
+ *   n_nodes    device, int32 [B], each 0 .. T, or NULL: T everywhere
+ *   tree_mask  device, uint64 [T] per sequence, mask_stride (0 or >= T)
+ *              elements apart: 0 is one tree for every sequence
+ *   caches     as tbq4_attn_decode, or pools and a block table as
+ *              tbq4_attn_decode_paged
+ *   workspace  device scratch of tbq4_tree_workspace_bytes(B, T, Hq, Hkv)
+ *              bytes, 256-byte aligned, for this call alone while it runs (two
+ *              calls that may overlap, or two graphs that may, need one each);
+ *              its size does not depend on the lengths
+ *   out        device, [B][T][Hq][128] of type out_dtype (TBQ4_F16 or
+ *              TBQ4_BF16, rounded to nearest even), 16-byte aligned
+ * The work is divided on the device from the lengths there, so one captured
+ * call serves any lengths and any number of nodes up to T.  A context below 0,
+ * a count outside 0 .. T, or ctx_lens[b] + n_nodes[b] above the capacity is
+ * clamped and flags TBQ4_ERR_CAPACITY in the device status, and so does a page
+ * id outside the pool (page 0 is read).
+ * Constraints: 1 <= B <= 1024, 1 <= T <= 64, Hq % Hkv == 0, Hq / Hkv <= 8.
+ * Precision: products of the cache's exact levels, sums and softmax
+ * statistics in binary32; queries and softmax weights enter the tensor cores
+ * as fp16 (TBQ4_BF16 outputs) or as pairs of fp16 terms (TBQ4_F16 outputs).
+ * Errors: TBQ4_ERR_NULL, TBQ4_ERR_ALIGN, TBQ4_ERR_SHAPE, TBQ4_ERR_CAPACITY,
+ * TBQ4_ERR_WORKSPACE, TBQ4_ERR_LAUNCH.
+ */
+TBQ4_API size_t tbq4_tree_workspace_bytes(int B, int T, int Hq, int Hkv);
+TBQ4_API tbq4_status tbq4_attn_tree(const void *q, int q_dtype, const uint8_t *k_cache,
+                                    const uint8_t *v_cache, const int32_t *ctx_lens,
+                                    const int32_t *n_nodes, const uint64_t *tree_mask,
+                                    int64_t mask_stride, int B, int T, int Hq, int Hkv,
+                                    int64_t capacity, float softmax_scale, uint64_t sign_seed,
+                                    void *workspace, size_t ws_bytes, void *out, int out_dtype,
+                                    void *stream);
+TBQ4_API tbq4_status tbq4_attn_tree_paged(const void *q, int q_dtype, const uint8_t *k_pool,
+                                          const uint8_t *v_pool, const int32_t *block_table,
+                                          int max_pages, int page_size, int64_t n_pages,
+                                          const int32_t *ctx_lens, const int32_t *n_nodes,
+                                          const uint64_t *tree_mask, int64_t mask_stride, int B,
+                                          int T, int Hq, int Hkv, float softmax_scale,
+                                          uint64_t sign_seed, void *workspace, size_t ws_bytes,
+                                          void *out, int out_dtype, void *stream);
+
+/*
+ * Acceptance: in every given cache, for every sequence b and KV head,
+ *   block[ctx_lens[b] + i] = old block[ctx_lens[b] + path[b][i]],
+ *   i < n_accept[b],
+ * and new_lens[b] = ctx_lens[b] + n_accept[b].  path[b] lists nodes in the
+ * order in which they are to follow the context (a path from the root in
+ * practice; any list is allowed, also with repeats).  Blocks from
+ * new_lens[b] on are left as they are.
+ *   k_caches,
+ *   v_caches  host arrays of n_layers device pointers, each cache (or pool) as
+ *             tbq4_attn_decode's and all distinct; they are read during the
+ *             call only
+ *   path      device, int32 [B][max_path], 1 <= max_path <= 64
+ *   n_accept  device, int32 [B], each 0 .. max_path
+ *   new_lens  device, int32 [B], or NULL; not ctx_lens
+ * A count outside 0 .. max_path, or a context that leaves no room for it,
+ * moves nothing of that sequence (its new length is its old one); a node whose
+ * slot or page lies outside the cache is skipped.  Both flag
+ * TBQ4_ERR_CAPACITY in the device status.
+ * Errors: TBQ4_ERR_NULL, TBQ4_ERR_ALIGN, TBQ4_ERR_SHAPE (sizes, a cache given
+ * twice, new_lens == ctx_lens), TBQ4_ERR_CAPACITY, TBQ4_ERR_LAUNCH.
+ */
+TBQ4_API tbq4_status tbq4_tree_accept(uint8_t *const *k_caches, uint8_t *const *v_caches,
+                                      int n_layers, const int32_t *ctx_lens, const int32_t *path,
+                                      const int32_t *n_accept, int max_path, int B, int Hkv,
+                                      int64_t capacity, int32_t *new_lens, void *stream);
+TBQ4_API tbq4_status tbq4_tree_accept_paged(uint8_t *const *k_pools, uint8_t *const *v_pools,
+                                            int n_layers, const int32_t *block_table, int max_pages,
+                                            int page_size, int64_t n_pages, const int32_t *ctx_lens,
+                                            const int32_t *path, const int32_t *n_accept,
+                                            int max_path, int B, int Hkv, int32_t *new_lens,
+                                            void *stream);
+
 /* Profiling hook (the page has no counterpart; it serves the measurement
  * of the kernels above): while set, every attention call records `before` on its
  * stream just before its attention kernel and `after` just after it, so a

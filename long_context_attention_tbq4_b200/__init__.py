@@ -10,6 +10,7 @@ indices) in a Hadamard-rotated domain, and attention dequantises the raw
 blocks inside its inner loop (trefon.com, "Kontekst 262K na jednej RTX 4090:
 co dodalem do llama.cpp-turboq", section "Od czego zaczalem").
 """
+import contextlib
 import ctypes as C
 
 import numpy as np
@@ -30,6 +31,8 @@ __all__ = [
     "empty_cache",
     "empty_pool", "tbq4_quantize_append_paged", "tbq4_attn_decode_paged",
     "BLOCK_BYTES3", "empty_cache3", "tbq3_quantize_append", "tbq3_attn_decode",
+    "tbq4_rope_append", "tbq4_rope_append_paged", "tree_mask", "tbq4_tree_workspace_bytes",
+    "tbq4_attn_tree", "tbq4_attn_tree_paged", "tbq4_tree_accept", "tbq4_tree_accept_paged",
 ]
 
 
@@ -327,6 +330,280 @@ def tbq4_attn_prefill_chunk(q, n_cached, k_cache, v_cache, softmax_scale, sign_s
         workspace.numel() * workspace.element_size(), _ptr(out), _stream(stream)),
         "tbq4_attn_prefill_chunk")
     return out
+
+
+# ---- speculative decoding with draft trees ---------------------------------
+
+_DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}    # tbq4_dtype
+
+
+def _one_device(first, *rest):
+    """The device that every given tensor (None: not given) lies on."""
+    for t in rest:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device}: one device is needed")
+    return first.device
+
+
+def _on(device):
+    """Makes `device` current for a call whose tensors lie on another one."""
+    if device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _stream_on(stream, device):
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"stream on {stream.device}, tensors on {device}")
+    return stream.cuda_stream
+
+
+def _ptr_or_null(t):
+    return t.data_ptr() if t is not None else None
+
+
+def _need_rows(t, name, dtype=None, heads=None, tokens=None):
+    """Rows of 128 at any token and head stride; returns those strides."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype not in _DTYPES or (dtype is not None and t.dtype != dtype):
+        raise TypeError(f"{name} must be {dtype or 'float32, float16 or bfloat16'}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[2] != D or t.stride(2) != 1:
+        raise ValueError(f"{name} must be [tokens][heads][128] with adjacent channels, "
+                         f"got {tuple(t.shape)} with strides {t.stride()}")
+    if (heads is not None and t.shape[1] != heads) or (tokens is not None and t.shape[0] != tokens):
+        raise ValueError(f"{name} must be [{tokens}][{heads}][128], got {tuple(t.shape)}")
+    # the stride of a dimension of one is never used
+    return (t.stride(0) if t.shape[0] > 1 else 0), (t.stride(1) if t.shape[1] > 1 else 0)
+
+
+def _rope_append(name, k, v, slots, inv_freq, kc, vc, Hkv, B, layout, table, q, positions, seq_ids,
+                 interleaved, sign_seed, q_out, stream):
+    k_tok, k_head = _need_rows(k, "k", heads=Hkv)
+    n = k.shape[0]
+    v_tok, v_head = _need_rows(v, "v", k.dtype, Hkv, n)
+    _need(slots, torch.int32, "slots", 1)
+    rot = 0
+    if inv_freq is not None:
+        _need(inv_freq, torch.float64, "inv_freq", 1)
+        rot = 2 * inv_freq.shape[0]
+    for t, what in ((positions, "positions"), (seq_ids, "seq_ids")):
+        if t is not None:
+            _need(t, torch.int32, what, 1)
+            if t.shape[0] != n:
+                raise ValueError(f"{what} must be [{n}], got {tuple(t.shape)}")
+    if slots.shape[0] != n:
+        raise ValueError(f"slots must be [{n}], got {tuple(slots.shape)}")
+    Hq = q_tok = q_head = 0
+    if q is not None:
+        q_tok, q_head = _need_rows(q, "q", k.dtype, tokens=n)
+        Hq = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty((n, Hq, D), dtype=q.dtype, device=q.device)
+        _need(q_out, q.dtype, "q_out", 3)
+        if q_out.shape != q.shape:
+            raise ValueError(f"q_out must be {tuple(q.shape)}, got {tuple(q_out.shape)}")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    device = _one_device(k, v, slots, inv_freq, kc, vc, table, q, positions, seq_ids, q_out)
+    with _on(device):
+        check(getattr(lib, name)(
+            _ptr_or_null(q), q_tok, q_head, k.data_ptr(), k_tok, k_head, v.data_ptr(), v_tok, v_head,
+            _DTYPES[k.dtype], n, B, Hq, Hkv, _ptr_or_null(seq_ids), slots.data_ptr(),
+            _ptr_or_null(positions), _ptr_or_null(inv_freq), rot, int(bool(interleaved)), *layout,
+            sign_seed, kc.data_ptr(), vc.data_ptr(), _ptr_or_null(q_out),
+            _stream_on(stream, device)), name)
+    return q_out
+
+
+def tbq4_rope_append(k, v, slots, inv_freq, k_cache, v_cache, q=None, positions=None, seq_ids=None,
+                     interleaved=False, sign_seed=0, q_out=None, stream=None):
+    """Rotary embedding of q and k and quantise-append of k and v, in one
+    launch.  k, v [n][Hkv][128] and q [n][Hq][128] in float32, float16 or
+    bfloat16, at any token and head stride that is a multiple of 16 bytes;
+    slots, positions (default: the slots), seq_ids (default: n / B tokens of
+    each sequence in turn; negative: padding) int32 [n]; inv_freq float64
+    [rot_dim / 2] (None: no rotation); caches uint8 [B][Hkv][capacity][66]
+    (written).  Returns the rotated queries, [n][Hq][128] in q's dtype (None
+    without q)."""
+    _need(k_cache, torch.uint8, "k_cache", 4)
+    _need(v_cache, torch.uint8, "v_cache", 4)
+    B, Hkv, cap, nb = k_cache.shape
+    if nb != BLOCK_BYTES or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must be [B][Hkv][capacity][66]")
+    return _rope_append("tbq4_rope_append", k, v, slots, inv_freq, k_cache, v_cache, Hkv, B, (cap,),
+                        None, q, positions, seq_ids, interleaved, sign_seed, q_out, stream)
+
+
+def tbq4_rope_append_paged(k, v, slots, inv_freq, block_table, k_pool, v_pool, q=None,
+                           positions=None, seq_ids=None, interleaved=False, sign_seed=0, q_out=None,
+                           stream=None):
+    """As tbq4_rope_append, into page pools uint8 [n_pages][Hkv][page_size][66]
+    through block_table int32 [B][max_pages]."""
+    _need(block_table, torch.int32, "block_table", 2)
+    n_pages, Hkv, page_size = _pool_shape(k_pool, "k_pool")
+    _pool_shape(v_pool, "v_pool")
+    if v_pool.shape != k_pool.shape:
+        raise ValueError("k_pool and v_pool differ in shape")
+    return _rope_append("tbq4_rope_append_paged", k, v, slots, inv_freq, k_pool, v_pool, Hkv,
+                        block_table.shape[0],
+                        (block_table.data_ptr(), block_table.shape[1], page_size, n_pages),
+                        block_table, q, positions, seq_ids, interleaved, sign_seed, q_out, stream)
+
+
+def tree_mask(parents):
+    """The masks of draft trees for tbq4_attn_tree: parents [T] or [B][T]
+    (integers, -1 for a node that hangs off the context) -> int64 of the same
+    shape and device, bit j of node i set where j is i or an ancestor of i."""
+    parents = torch.as_tensor(parents).long()
+    T = parents.shape[-1]
+    if not 1 <= T <= 64:
+        raise ValueError(f"1 to 64 nodes, got {T}")
+    if bool(((parents < -1) | (parents >= T)).any()):
+        raise ValueError("a parent is a node of the tree or -1")
+    node = torch.arange(T, device=parents.device)
+    sees = torch.zeros((*parents.shape, T), dtype=torch.bool, device=parents.device)
+    at = node.expand_as(parents)
+    for _ in range(T):                         # one generation at a time
+        sees |= at[..., None] == node
+        at = torch.where(at >= 0, parents.gather(-1, at.clamp(min=0)), -1)
+    if bool((at >= 0).any()):
+        raise ValueError("the parents run in a circle")
+    return torch.where(sees, torch.ones_like(node) << node, 0).sum(-1)
+
+
+def tbq4_tree_workspace_bytes(B, T, Hq, Hkv) -> int:
+    return int(lib.tbq4_tree_workspace_bytes(B, T, Hq, Hkv))
+
+
+def _attn_tree(name, q, kc, vc, Hkv, layout, table, ctx_lens, mask, softmax_scale, sign_seed, n_nodes,
+               workspace, out, out_dtype, stream):
+    if not isinstance(q, torch.Tensor) or q.dtype not in _DTYPES:
+        raise TypeError("q must be a float32, float16 or bfloat16 CUDA tensor")
+    _need(q, q.dtype, "q", 4)
+    _need(ctx_lens, torch.int32, "ctx_lens", 1)
+    _need(mask, torch.int64, "tree_mask")
+    B, T, Hq, d = q.shape
+    if d != D or ctx_lens.shape[0] != B:
+        raise ValueError("shape mismatch between q, caches and ctx_lens")
+    if tuple(mask.shape) not in ((T,), (B, T)):
+        raise ValueError(f"tree_mask must be [{T}] or [{B}][{T}], got {tuple(mask.shape)}")
+    if n_nodes is not None:
+        _need(n_nodes, torch.int32, "n_nodes", 1)
+        if n_nodes.shape[0] != B:
+            raise ValueError(f"n_nodes must be [{B}], got {tuple(n_nodes.shape)}")
+    if workspace is None:
+        workspace = torch.empty(max(tbq4_tree_workspace_bytes(B, T, Hq, Hkv), 1), dtype=torch.uint8,
+                                device=q.device)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    if out is None:
+        if out_dtype is None:
+            out_dtype = torch.bfloat16 if q.dtype == torch.bfloat16 else torch.float16
+        out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
+    if out.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError(f"out must be float16 or bfloat16, got {out.dtype}")
+    _need(out, out.dtype, "out", 4)
+    if out.shape != q.shape:
+        raise ValueError(f"out must be {tuple(q.shape)}, got {tuple(out.shape)}")
+    device = _one_device(q, kc, vc, table, ctx_lens, mask, n_nodes, workspace, out)
+    with _on(device):
+        check(getattr(lib, name)(
+            q.data_ptr(), _DTYPES[q.dtype], kc.data_ptr(), vc.data_ptr(), *(layout if table is not None else ()),
+            ctx_lens.data_ptr(), _ptr_or_null(n_nodes), mask.data_ptr(), T if mask.dim() == 2 else 0,
+            B, T, Hq, Hkv, *(layout if table is None else ()), float(softmax_scale), sign_seed,
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), out.data_ptr(),
+            _DTYPES[out.dtype], _stream_on(stream, device)), name)
+    return out
+
+
+def tbq4_attn_tree(q, k_cache, v_cache, ctx_lens, tree_mask, softmax_scale, sign_seed=0, n_nodes=None,
+                   workspace=None, out=None, out_dtype=None, stream=None):
+    """Attention of drafted nodes over their context and tree: q [B][T][Hq][128]
+    in float32, float16 or bfloat16; caches uint8 [B][Hkv][capacity][66] that
+    hold ctx_lens[b] tokens and the nodes right behind them; ctx_lens, n_nodes
+    (default: T everywhere) int32 [B]; tree_mask int64 [B][T] or [T] (one tree
+    for all): bit j of entry i set where node i sees node j.  Returns
+    [B][T][Hq][128] in out's dtype (default: bfloat16 for bfloat16 queries,
+    else float16); rows of nodes >= n_nodes[b] are not written."""
+    _need(k_cache, torch.uint8, "k_cache", 4)
+    _need(v_cache, torch.uint8, "v_cache", 4)
+    B, Hkv, cap, nb = k_cache.shape
+    if nb != BLOCK_BYTES or v_cache.shape != k_cache.shape or B != q.shape[0]:
+        raise ValueError("shape mismatch between q and caches")
+    return _attn_tree("tbq4_attn_tree", q, k_cache, v_cache, Hkv, (cap,), None, ctx_lens, tree_mask,
+                      softmax_scale, sign_seed, n_nodes, workspace, out, out_dtype, stream)
+
+
+def tbq4_attn_tree_paged(q, k_pool, v_pool, block_table, ctx_lens, tree_mask, softmax_scale,
+                         sign_seed=0, n_nodes=None, workspace=None, out=None, out_dtype=None,
+                         stream=None):
+    """As tbq4_attn_tree, over page pools uint8 [n_pages][Hkv][page_size][66]
+    through block_table int32 [B][max_pages]."""
+    _need(block_table, torch.int32, "block_table", 2)
+    n_pages, Hkv, page_size = _pool_shape(k_pool, "k_pool")
+    _pool_shape(v_pool, "v_pool")
+    if v_pool.shape != k_pool.shape or block_table.shape[0] != q.shape[0]:
+        raise ValueError("shape mismatch between q, block_table and pools")
+    return _attn_tree("tbq4_attn_tree_paged", q, k_pool, v_pool, Hkv,
+                      (block_table.data_ptr(), block_table.shape[1], page_size, n_pages), block_table,
+                      ctx_lens, tree_mask, softmax_scale, sign_seed, n_nodes, workspace, out,
+                      out_dtype, stream)
+
+
+def _tree_accept(name, ks, vs, shape, B, Hkv, layout, table, ctx_lens, path, n_accept, new_lens, stream):
+    if len(ks) != len(vs) or not ks:
+        raise ValueError(f"{len(ks)} K and {len(vs)} V caches: as many of each, at least one")
+    for c in (*ks, *vs):
+        _need(c, torch.uint8, "each cache", 4)
+        if c.shape != shape:
+            raise ValueError("the caches differ in shape")
+    _need(ctx_lens, torch.int32, "ctx_lens", 1)
+    _need(path, torch.int32, "path", 2)
+    _need(n_accept, torch.int32, "n_accept", 1)
+    if new_lens is None:
+        new_lens = torch.empty_like(ctx_lens)
+    _need(new_lens, torch.int32, "new_lens", 1)
+    if not B == ctx_lens.shape[0] == path.shape[0] == n_accept.shape[0] == new_lens.shape[0]:
+        raise ValueError("shape mismatch between caches, ctx_lens, path, n_accept and new_lens")
+    device = _one_device(ctx_lens, path, n_accept, new_lens, table, *ks, *vs)
+    n = len(ks)
+    with _on(device):
+        check(getattr(lib, name)(
+            (C.c_void_p * n)(*[c.data_ptr() for c in ks]), (C.c_void_p * n)(*[c.data_ptr() for c in vs]),
+            n, *(layout if table is not None else ()), ctx_lens.data_ptr(), path.data_ptr(),
+            n_accept.data_ptr(), path.shape[1], B, Hkv, *(layout if table is None else ()),
+            new_lens.data_ptr(), _stream_on(stream, device)), name)
+    return new_lens
+
+
+def tbq4_tree_accept(k_caches, v_caches, ctx_lens, path, n_accept, new_lens=None, stream=None):
+    """Keeps the accepted nodes in every layer's caches (lists of uint8
+    [B][Hkv][capacity][66], written): block ctx_lens[b] + i becomes block
+    ctx_lens[b] + path[b][i] for i < n_accept[b].  path int32 [B][max_path],
+    ctx_lens and n_accept int32 [B].  Returns the new lengths, int32 [B]."""
+    _need(k_caches[0], torch.uint8, "each cache", 4)
+    shape = k_caches[0].shape
+    if shape[3] != BLOCK_BYTES:
+        raise ValueError("caches must be [B][Hkv][capacity][66]")
+    return _tree_accept("tbq4_tree_accept", k_caches, v_caches, shape, shape[0], shape[1], (shape[2],),
+                        None, ctx_lens, path, n_accept, new_lens, stream)
+
+
+def tbq4_tree_accept_paged(k_pools, v_pools, block_table, ctx_lens, path, n_accept, new_lens=None,
+                           stream=None):
+    """As tbq4_tree_accept, over page pools (lists of uint8
+    [n_pages][Hkv][page_size][66]) that share block_table int32 [B][max_pages]."""
+    _need(block_table, torch.int32, "block_table", 2)
+    n_pages, Hkv, page_size = _pool_shape(k_pools[0], "each pool")
+    return _tree_accept("tbq4_tree_accept_paged", k_pools, v_pools, k_pools[0].shape,
+                        block_table.shape[0], Hkv,
+                        (block_table.data_ptr(), block_table.shape[1], page_size, n_pages), block_table,
+                        ctx_lens, path, n_accept, new_lens, stream)
 
 
 def tbq4_set_timing_events(before=None, after=None):

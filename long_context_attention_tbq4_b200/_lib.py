@@ -44,6 +44,18 @@ SIGNATURES = {
     "tbq4_prefill_workspace_bytes": (_sz, [_i, _i, _i, _i64]),
     "tbq4_attn_prefill_chunk": (_i, [_p, _i, _i64, _p, _p, _i, _i, _i64, _f,
                                      _u64, _p, _sz, _p, _p]),
+    "tbq4_rope_append": (_i, [_p, _i64, _i64, _p, _i64, _i64, _p, _i64, _i64, _i, _i, _i, _i, _i,
+                              _p, _p, _p, _p, _i, _i, _i64, _u64, _p, _p, _p, _p]),
+    "tbq4_rope_append_paged": (_i, [_p, _i64, _i64, _p, _i64, _i64, _p, _i64, _i64, _i, _i, _i, _i,
+                                    _i, _p, _p, _p, _p, _i, _i, _p, _i, _i, _i64, _u64, _p, _p, _p,
+                                    _p]),
+    "tbq4_tree_workspace_bytes": (_sz, [_i, _i, _i, _i]),
+    "tbq4_attn_tree": (_i, [_p, _i, _p, _p, _p, _p, _p, _i64, _i, _i, _i, _i, _i64, _f, _u64, _p,
+                            _sz, _p, _i, _p]),
+    "tbq4_attn_tree_paged": (_i, [_p, _i, _p, _p, _p, _i, _i, _i64, _p, _p, _p, _i64, _i, _i, _i,
+                                  _i, _f, _u64, _p, _sz, _p, _i, _p]),
+    "tbq4_tree_accept": (_i, [_p, _p, _i, _p, _p, _p, _i, _i, _i, _i64, _p, _p]),
+    "tbq4_tree_accept_paged": (_i, [_p, _p, _i, _p, _i, _i, _i64, _p, _p, _p, _i, _i, _i, _p, _p]),
     "tbq4_set_timing_events": (None, [_p, _p]),
     "tbq4_get_device_status": (_i, [_p]),
     "tbq4_selftest_bounded_wait": (_i, [C.c_uint32, _p]),

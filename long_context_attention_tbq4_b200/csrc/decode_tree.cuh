@@ -1,0 +1,361 @@
+// decode_tree.cuh -- attention of a tree of drafted tokens over TBQ4 caches:
+// parameters, work schedule and the join of split rows.
+//
+// Sequence b holds ctx_b cached tokens and, in the slots right behind them,
+// the n_b nodes of a draft tree.  Node i sees every cached token and the
+// nodes whose bits are set in its mask:
+//
+//   O_i = sum_t p_it v_t / sum_t p_it,  p_it = exp(scale q_i . k_t),
+//   t in [0, ctx_b) and ctx_b + {j < n_b : bit j of mask_bi}
+//
+// over the raw blocks, in the rotated domain (trefon.com, "Kontekst 262K na
+// jednej RTX 4090", section "Od czego zaczalem"; drafted tokens: section
+// "Konfiguracja").  A row that sees nothing is 0.
+//
+// Work.  The G heads of a KV head and the nodes make n_b G query rows that
+// read the same keys; they go in blocks of up to kRows rows (row c of the
+// sequence's rows = node c / G, head c % G).  A work is one (sequence, KV
+// head, row block) over all of its 128-token tiles.  The tiles of all works
+// are numbered through, and the grid's CTAs (one per SM) take equal
+// consecutive shares, so ragged batches balance whatever the lengths on the
+// device are, and one captured launch serves any lengths.  A CTA that holds
+// a whole work writes its rows; a work that crosses CTAs leaves one partial
+// (O_rot, m, l) per CTA, which tree_combine_kernel joins by log-sum-exp.
+#pragma once
+#include "common.cuh"
+#include "decode.cuh"
+#include "rope_append.cuh"
+
+namespace tbq4 {
+namespace tree {
+
+constexpr int kTileT = 128;                 // tokens per tile
+constexpr int kMaxNodes = 64;
+constexpr int kMaxBatch = 1024;             // prefix sums in shared memory
+
+struct TreeParams {
+    const void *q;                          // [B][T][Hq][128]
+    int q_type;                             // ElemType
+    const uint8_t *k, *v;                   // caches or pools
+    int64_t capacity;                       // tokens a sequence can hold
+    int64_t seq_stride, head_stride;        // bytes (contiguous caches)
+    const int32_t *table;                   // nullptr: contiguous
+    int max_pages, page_size;
+    int64_t n_pages;
+    const int32_t *ctx_lens, *n_nodes;      // n_nodes may be nullptr: T
+    const unsigned long long *mask;         // [B][T], or [T] with mask_stride 0
+    int64_t mask_stride;
+    int B, T, Hq, Hkv, G;
+    int rows;                               // rows per block
+    float scale;
+    uint64_t sign_lo, sign_hi;
+    float *part_o;                          // [2 n_ctas][rows][128]
+    float2 *part_ml;                        // [2 n_ctas][rows]: max (log2 units), sum
+    int n_ctas;
+    void *out;                              // [B][T][Hq][128]
+    int out_type;
+    int64_t cache_bytes, out_elems;         // extents, for the debug build's bounds checks
+};
+
+// Tokens and nodes of sequence b, clamped to what its cache can hold.
+__device__ __forceinline__ void seq_extent(const TreeParams &p, int b, int &ctx, int &n) {
+    ctx = __ldg(p.ctx_lens + b);
+    n = p.n_nodes ? __ldg(p.n_nodes + b) : p.T;
+    bool bad = n < 0 || n > p.T || ctx < 0;
+    n = min(max(n, 0), p.T);
+    ctx = max(ctx, 0);
+    if ((int64_t)ctx + n > p.capacity) {
+        bad = true;
+        n = (int)min((int64_t)n, p.capacity);
+        ctx = (int)min((int64_t)ctx, p.capacity - n);
+    }
+    if (bad) record_status(4u /* TBQ4_ERR_CAPACITY */);
+}
+
+// Tiles and row blocks of a sequence with ctx cached tokens and n nodes.
+__device__ __forceinline__ int seq_tiles(int ctx, int n) {
+    return n > 0 ? (int)(((int64_t)ctx + n + kTileT - 1) / kTileT) : 0;
+}
+__device__ __forceinline__ int seq_blocks(const TreeParams &p, int n) {
+    return (n * p.G + p.rows - 1) / p.rows;
+}
+
+// prefix[b] = units (tiles of all works) of the sequences before b, b <= B,
+// by the first warps of the CTA; every thread of the CTA calls it.  The host
+// bounds the total below 2^31.
+__device__ __forceinline__ void build_prefix(const TreeParams &p, int *prefix) {
+    for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
+        int ctx, n;
+        seq_extent(p, b, ctx, n);
+        prefix[b + 1] = seq_tiles(ctx, n) * seq_blocks(p, n) * p.Hkv;
+    }
+    if (threadIdx.x == 0) prefix[0] = 0;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x, per = (p.B + 31) / 32;
+        const int b0 = min(lane * per, p.B), b1 = min(b0 + per, p.B);
+        int sum = 0;
+        for (int b = b0; b < b1; ++b) sum += prefix[b + 1];
+        int base = sum;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const int o = __shfl_up_sync(kFull, base, m);
+            if (lane >= m) base += o;
+        }
+        base -= sum;
+        for (int b = b0; b < b1; ++b) {
+            base += prefix[b + 1];
+            prefix[b + 1] = base;
+        }
+    }
+    __syncthreads();
+}
+
+// CTAs that get a share (each of at least one unit), the first unit of share
+// c, and the share that holds unit u.
+__device__ __forceinline__ int n_shares(const TreeParams &p, int units) { return min(p.n_ctas, units); }
+__device__ __forceinline__ int share_begin(int units, int c, int shares) {
+    return (int)((int64_t)units * c / shares);
+}
+__device__ __forceinline__ int share_of(int units, int u, int shares) {
+    return (int)((((int64_t)u + 1) * shares - 1) / units);
+}
+
+// One CTA's run of tiles inside one work.
+struct Segment {
+    int b, g, blk;                          // sequence, KV head, row block
+    int ctx, n;                             // its cached tokens and nodes
+    int tile0, tiles;                       // tiles of this run
+    int row0, rows;                         // rows of the block
+    int begin, work_tiles;                  // the work's first unit, and its units
+};
+
+// The segment that starts at unit u and ends at the work's end or at `end`.
+__device__ __forceinline__ Segment segment_at(const TreeParams &p, const int *prefix, int u, int end) {
+    int lo = 0, hi = p.B - 1;               // the last b with prefix[b] <= u
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (prefix[mid] <= u) lo = mid; else hi = mid - 1;
+    }
+    Segment s;
+    s.b = lo;
+    seq_extent(p, s.b, s.ctx, s.n);
+    s.work_tiles = seq_tiles(s.ctx, s.n);
+    const int blocks = seq_blocks(p, s.n), local = u - prefix[s.b];
+    const int w = local / s.work_tiles;
+    s.tile0 = local - w * s.work_tiles;
+    s.begin = prefix[s.b] + w * s.work_tiles;
+    s.tiles = min(s.work_tiles - s.tile0, end - u);
+    s.g = w / blocks;
+    s.blk = w - s.g * blocks;
+    // rows spread evenly over the blocks, in whole eights
+    const int all = s.n * p.G, per = ((all + blocks - 1) / blocks + 7) & ~7;
+    s.row0 = s.blk * per;
+    s.rows = max(0, min(per, all - s.row0));
+    return s;
+}
+// Where a partial of CTA c goes: its first run when that starts inside a
+// work, its last when that ends inside one.
+__device__ __forceinline__ int part_slot(const Segment &s, int c) { return 2 * c + (s.tile0 == 0); }
+
+// o = D H o_rot / sqrt(128) of one normalised row held four values per lane,
+// rounded to the output's type and stored (row c of the work's sequence).
+__device__ __forceinline__ void store_out(const TreeParams &p, int b, int g, int c, float (&v)[4],
+                                          int lane) {
+    warp_fwht128(v, lane);
+    const uint32_t sbits = lane_sign_bits(p.sign_lo, p.sign_hi, lane);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        v[k] *= rot_c();
+        if ((sbits >> k) & 1u) v[k] = -v[k];
+    }
+    const int i = c / p.G, h = g * p.G + (c - i * p.G);
+    const int64_t oi = (((int64_t)b * p.T + i) * p.Hq + h) * kD + 4 * lane;
+    if (in_extent(oi, 4, p.out_elems)) store4(p.out, p.out_type, oi, v);
+}
+
+// Joins the works that cross CTAs.  grid.x walks the starts of shares 1 .. : a
+// start that lies inside a work, and is the first such start, owns the work.
+// Four warps per row take every fourth partial with a running maximum, and
+// the four results meet in shared memory.
+constexpr int kJoinWarps = 4, kJoinRows = 4;
+
+__global__ void __launch_bounds__(kJoinWarps * kJoinRows * 32)
+tree_combine_kernel(const TreeParams p) {
+    __shared__ int prefix[kMaxBatch + 1];
+    __shared__ float4 o_s[kJoinRows][kJoinWarps][32];
+    __shared__ float2 ml_s[kJoinRows][kJoinWarps];
+    build_prefix(p, prefix);                // reads the lengths: inputs, not results
+    // every CTA waits, also one that then has nothing to do: a kernel after
+    // this one may start once this grid has ended
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int units = prefix[p.B], shares = n_shares(p, units);
+    const int c1 = blockIdx.x + 1;
+    if (c1 >= shares) return;
+    const int u = share_begin(units, c1, shares);
+    const Segment s = segment_at(p, prefix, u, units);
+    const int first = share_of(units, s.begin, shares);
+    const int last = share_of(units, s.begin + s.work_tiles - 1, shares);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int sub = warp % kJoinWarps, ri = warp / kJoinWarps;
+    const int r = blockIdx.y * kJoinRows + ri;
+    if (u == s.begin || first != c1 - 1 || (int)blockIdx.y * kJoinRows >= s.rows) return;
+    float M = -INFINITY, L = 0.f;
+    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < s.rows) {
+#pragma unroll 4
+        for (int c = first + sub; c <= last; c += kJoinWarps) {
+            const int64_t row = (int64_t)(2 * c + (c == first)) * p.rows + r;
+            const float2 ml = __ldcg(p.part_ml + row);
+            const float4 o = __ldcg(reinterpret_cast<const float4 *>(p.part_o + row * kD) + lane);
+            if (ml.y == 0.f) continue;      // the run's tokens are all invisible to this row
+            const float Mn = fmaxf(M, ml.x);
+            const float a = exp2f(M - Mn), w = exp2f(ml.x - Mn);
+            O.x = O.x * a + o.x * w;
+            O.y = O.y * a + o.y * w;
+            O.z = O.z * a + o.z * w;
+            O.w = O.w * a + o.w * w;
+            L = L * a + ml.y * w;
+            M = Mn;
+        }
+    }
+    o_s[ri][sub][lane] = O;
+    if (lane == 0) ml_s[ri][sub] = make_float2(M, L);
+    __syncthreads();
+    if (sub != 0 || r >= s.rows) return;
+    float Mt = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) Mt = fmaxf(Mt, ml_s[ri][w].x);
+    float v[4] = {0.f, 0.f, 0.f, 0.f}, Lt = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+        const float2 ml = ml_s[ri][w];
+        if (ml.y == 0.f) continue;
+        const float f = exp2f(ml.x - Mt);
+        const float4 o = o_s[ri][w][lane];
+        v[0] += f * o.x;
+        v[1] += f * o.y;
+        v[2] += f * o.z;
+        v[3] += f * o.w;
+        Lt += f * ml.y;
+    }
+    const float inv = Lt == 0.f ? 0.f : 1.0f / Lt;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] *= inv;
+    store_out(p, s.b, s.g, s.row0 + r, v, lane);
+}
+
+// Byte offset of 32-token piece `t` (a multiple of 32) of (b, g) in either
+// cache.  A page id outside the pool reads page 0 and is flagged.
+__device__ __forceinline__ int64_t piece_offset(const TreeParams &p, int b, int g, int32_t t) {
+    if (!p.table) return b * p.seq_stride + g * p.head_stride + (int64_t)t * kBlockBytes;
+    int32_t pid = __ldg(p.table + (int64_t)b * p.max_pages + t / p.page_size);
+    if (pid < 0 || (int64_t)pid >= p.n_pages) {
+        record_status(4u /* TBQ4_ERR_CAPACITY */);
+        pid = 0;
+    }
+    return (((int64_t)pid * p.Hkv + g) * p.page_size + t % p.page_size) * kBlockBytes;
+}
+
+// Plain kernel: 32 tokens at a time dequantised into shared memory, fp32
+// products on the CUDA cores.  A warp owns four of the block's rows: lane =
+// token for the scores, lane = four dimensions for the output.
+constexpr int kPlainRows = 32, kPlainWarps = 8;
+constexpr int kPlainSmem = (3 * 32 * (kD + 1)) * 4;
+
+__global__ void __launch_bounds__(kPlainWarps * 32)
+tree_plain_kernel(const TreeParams p) {
+    extern __shared__ float sm[];
+    __shared__ int prefix[kMaxBatch + 1];
+    float *qs = sm, *ks = sm + 32 * (kD + 1), *vs = ks + 32 * (kD + 1);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    build_prefix(p, prefix);
+    const int units = prefix[p.B], shares = n_shares(p, units), cta = blockIdx.x;
+    if (cta >= shares) return;
+    int u = share_begin(units, cta, shares);
+    const int end = share_begin(units, cta + 1, shares);
+    const uint32_t sbits = lane_sign_bits(p.sign_lo, p.sign_hi, lane);
+    const float c = p.scale * 1.4426950408889634f;
+    while (u < end) {
+        const Segment s = segment_at(p, prefix, u, end);
+        u += s.tiles;
+        __syncthreads();
+        for (int r = warp; r < 32; r += kPlainWarps) {
+            float v[4] = {0.f, 0.f, 0.f, 0.f};
+            if (r < s.rows) {
+                const int row = s.row0 + r, i = row / p.G, h = s.g * p.G + row % p.G;
+                load4(p.q, p.q_type, (((int64_t)s.b * p.T + i) * p.Hq + h) * kD + 4 * lane, v);
+                warp_rotate128(v, sbits, lane);
+            }
+            for (int k = 0; k < 4; ++k) qs[r * (kD + 1) + 4 * lane + k] = v[k] * c;
+        }
+        float m[4], l[4];
+        float o[4][4] = {};
+        unsigned long long mask[4];
+        for (int k = 0; k < 4; ++k) {
+            const int row = s.row0 + 4 * warp + k;
+            m[k] = -INFINITY;
+            l[k] = 0.f;
+            mask[k] = 4 * warp + k < s.rows ? p.mask[s.b * p.mask_stride + row / p.G] : 0ull;
+        }
+        const int stop = min((s.tile0 + s.tiles) * kTileT, s.ctx + s.n);
+        for (int t0 = s.tile0 * kTileT; t0 < stop; t0 += 32) {
+            __syncthreads();
+            const int64_t off = piece_offset(p, s.b, s.g, t0);
+            for (int e = threadIdx.x; e < 2 * 32 * 64; e += blockDim.x) {
+                const int which = e >> 11, t = (e >> 6) & 31, j = e & 63;
+                float *dst = (which ? vs : ks) + t * (kD + 1) + 2 * j;
+                float lo = 0.f, hi = 0.f;
+                const int64_t o1 = off + (int64_t)t * kBlockBytes;
+                if (t0 + t < stop && in_extent(o1, kBlockBytes, p.cache_bytes)) {
+                    const uint8_t *blk = (which ? p.v : p.k) + o1;
+                    const float S = half_bits_to_float(*reinterpret_cast<const uint16_t *>(blk)) / 15.0f;
+                    const int x = blk[2 + j];
+                    lo = S * (float)(2 * (x & 15) - 15);
+                    hi = S * (float)(2 * (x >> 4) - 15);
+                }
+                dst[0] = lo;
+                dst[1] = hi;
+            }
+            __syncthreads();
+            const int t = t0 + lane, j = t - s.ctx;
+            for (int k = 0; k < 4; ++k) {
+                const float *qr = qs + (4 * warp + k) * (kD + 1);
+                float x = 0.f;
+                for (int d = 0; d < kD; ++d) x = fmaf(qr[d], ks[lane * (kD + 1) + d], x);
+                const bool sees = t < stop && (j < 0 || ((mask[k] >> j) & 1ull));
+                if (!sees) x = -INFINITY;
+                const float mn = fmaxf(m[k], warp_max(x));
+                const float a = mn == -INFINITY ? 1.f : exp2f(m[k] - mn);
+                const float pr = sees ? exp2f(x - mn) : 0.f;
+                m[k] = mn;
+                l[k] = l[k] * a + warp_sum(pr);
+                for (int e = 0; e < 4; ++e) o[k][e] *= a;
+                for (int tt = 0; tt < 32; ++tt) {
+                    const float w = __shfl_sync(kFull, pr, tt);
+                    if (w == 0.f) continue;                  // a hidden token adds nothing, whatever it holds
+                    for (int e = 0; e < 4; ++e)
+                        o[k][e] = fmaf(w, vs[tt * (kD + 1) + 4 * lane + e], o[k][e]);
+                }
+            }
+        }
+        for (int k = 0; k < 4; ++k) {
+            const int r = 4 * warp + k;
+            if (r >= s.rows) continue;
+            if (s.tiles == s.work_tiles) {
+                const float inv = l[k] == 0.f ? 0.f : 1.0f / l[k];
+                float v[4] = {o[k][0] * inv, o[k][1] * inv, o[k][2] * inv, o[k][3] * inv};
+                store_out(p, s.b, s.g, s.row0 + r, v, lane);
+            } else {
+                const int64_t row = (int64_t)part_slot(s, cta) * p.rows + r;
+                reinterpret_cast<float4 *>(p.part_o + row * kD)[lane] =
+                    make_float4(o[k][0], o[k][1], o[k][2], o[k][3]);
+                if (lane == 0) p.part_ml[row] = make_float2(m[k], l[k]);
+            }
+        }
+    }
+}
+
+}  // namespace tree
+}  // namespace tbq4

@@ -11,10 +11,14 @@
 #include "decode_tc.cuh"
 #include "decode_mq.cuh"
 #include "prefill_tc.cuh"
+#include "rope_append.cuh"
+#include "decode_tree.cuh"
+#include "tree_accept.cuh"
 #include "selftest.cuh"
 
 #include <algorithm>
 #include <cmath>
+#include <functional>
 #include <mutex>
 
 #include <nvtx3/nvToolsExt.h>
@@ -665,6 +669,321 @@ tbq4_status tbq4_attn_prefill_chunk(const uint16_t *q, int n_new, int64_t n_cach
     if (cudaLaunchKernelEx(&cfg, combine_rows_kernel, c, n_rows) != cudaSuccess)
         return TBQ4_ERR_LAUNCH;
     return launch_status();
+}
+
+}  // extern "C"
+
+namespace {
+
+size_t elem_bytes(int dtype) { return dtype == TBQ4_F32 ? 4 : 2; }
+bool elem_type(int dtype) {
+    return dtype == TBQ4_F32 || dtype == TBQ4_F16 || dtype == TBQ4_BF16;
+}
+
+// A row's source: every row must start on a 16-byte boundary.
+struct Rows {
+    const void *p;
+    int64_t tok, head;
+    bool aligned16(int dtype) const {
+        const int64_t per = 16 / (int64_t)elem_bytes(dtype);
+        return aligned(p, 16) && tok >= 0 && head >= 0 && tok % per == 0 && head % per == 0;
+    }
+};
+
+tbq4_status rope_impl(const Rows &q, const Rows &k, const Rows &v, int dtype, int n_tokens, int B,
+                      int Hq, int Hkv, const int32_t *seq_ids, const int32_t *slots,
+                      const int32_t *positions, const double *inv_freq, int rot_dim,
+                      int interleaved, int64_t capacity, const PagedArgs *pg, uint64_t sign_seed,
+                      uint8_t *kc, uint8_t *vc, void *q_out, void *stream) {
+    const NvtxRange range(pg ? "tbq4_rope_append_paged" : "tbq4_rope_append");
+    if (!k.p || !v.p || !slots || !kc || !vc || (Hq > 0 && (!q.p || !q_out)) ||
+        (rot_dim > 0 && !inv_freq))
+        return TBQ4_ERR_NULL;
+    if (pg) {
+        const tbq4_status e = check_paged(*pg, &capacity);
+        if (e != TBQ4_OK) return e;
+    }
+    if (!elem_type(dtype)) return TBQ4_ERR_SHAPE;
+    if (!k.aligned16(dtype) || !v.aligned16(dtype) || (Hq > 0 && !q.aligned16(dtype)) ||
+        (Hq > 0 && !aligned(q_out, 16)) || !aligned(kc, 16) || !aligned(vc, 16) ||
+        !aligned(slots, 4) || !aligned(seq_ids, 4) || !aligned(positions, 4) ||
+        !aligned(inv_freq, 8))
+        return TBQ4_ERR_ALIGN;
+    if (n_tokens < 0 || B <= 0 || Hkv <= 0 || Hkv > 65535 || Hq < 0 || Hq > 65535 || rot_dim < 0 ||
+        rot_dim > kD || rot_dim % 8 != 0 || kc == vc || (!seq_ids && n_tokens % B != 0))
+        return TBQ4_ERR_SHAPE;
+    if (capacity <= 0 || capacity % 8 != 0) return TBQ4_ERR_CAPACITY;
+    if (n_tokens == 0) return TBQ4_OK;
+    RopeParams p = {};
+    p.q = q.p;
+    p.k = k.p;
+    p.v = v.p;
+    p.q_tok = q.tok;
+    p.q_head = q.head;
+    p.k_tok = k.tok;
+    p.k_head = k.head;
+    p.v_tok = v.tok;
+    p.v_head = v.head;
+    p.type = dtype;
+    p.n_tokens = n_tokens;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.B = B;
+    p.per_seq = seq_ids ? 1 : n_tokens / B;
+    p.seq_ids = seq_ids;
+    p.slots = slots;
+    p.positions = positions;
+    p.inv_freq = inv_freq;
+    p.rot = rot_dim;
+    p.interleaved = interleaved != 0;
+    p.capacity = capacity;
+    sign_words(sign_seed, &p.sign_lo, &p.sign_hi);
+    if (pg) {
+        p.pm.table = pg->block_table;
+        p.pm.max_pages = pg->max_pages;
+        p.pm.page_size = pg->page_size;
+        p.pm.n_pages = pg->n_pages;
+    }
+    p.pm.cache_bytes = (pg ? pg->n_pages * pg->page_size : (int64_t)B * capacity) * Hkv * kBlockBytes;
+    p.kc = kc;
+    p.vc = vc;
+    p.q_out = q_out;
+    p.q_out_elems = (int64_t)n_tokens * Hq * kD;
+    const int blocks = std::min(n_tokens, kNumSMs * 64);
+    rope_append_kernel<<<blocks, kRopeWarps * 32, 0, (cudaStream_t)stream>>>(p);
+    return launch_status();
+}
+
+// Rows per block of tree attention.
+int tree_rows(int) { return tree::kPlainRows; }
+
+size_t tree_ws_bytes(int rows) {
+    return align_up((size_t)2 * kNumSMs * rows * (kD * sizeof(float) + sizeof(float2)), kWsAlign);
+}
+
+tbq4_status tree_impl(const void *q, int q_dtype, const uint8_t *k, const uint8_t *v,
+                      const int32_t *ctx_lens, const int32_t *n_nodes, const uint64_t *mask,
+                      int64_t mask_stride, int B, int T, int Hq, int Hkv, int64_t capacity,
+                      const PagedArgs *pg, float softmax_scale, uint64_t sign_seed, void *workspace,
+                      size_t ws_bytes, void *out, int out_dtype, void *stream) {
+    const NvtxRange range(pg ? "tbq4_attn_tree_paged" : "tbq4_attn_tree");
+    if (!q || !k || !v || !ctx_lens || !mask || !workspace || !out) return TBQ4_ERR_NULL;
+    if (pg) {
+        const tbq4_status e = check_paged(*pg, &capacity);
+        if (e != TBQ4_OK) return e;
+    }
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(workspace, kWsAlign) ||
+        !aligned(out, 16) || !aligned(ctx_lens, 4) || !aligned(n_nodes, 4) || !aligned(mask, 8))
+        return TBQ4_ERR_ALIGN;
+    if (!elem_type(q_dtype) || (out_dtype != TBQ4_F16 && out_dtype != TBQ4_BF16) || B <= 0 ||
+        B > tree::kMaxBatch || T <= 0 || T > tree::kMaxNodes || Hkv <= 0 || Hkv > 65535 ||
+        Hq <= 0 || Hq % Hkv != 0 || Hq / Hkv > kMaxGroup || (mask_stride != 0 && mask_stride < T) ||
+        !std::isfinite(softmax_scale))
+        return TBQ4_ERR_SHAPE;
+    if (capacity <= 0 || capacity % 8 != 0 || capacity > INT32_MAX - 256) return TBQ4_ERR_CAPACITY;
+    const int rows = tree_rows(out_dtype);
+    // units (tiles of all works) are numbered in 32 bits
+    const int64_t most = ceil_div(capacity, tree::kTileT) * ceil_div((int64_t)T * (Hq / Hkv), rows) *
+                         Hkv;
+    if (most > INT32_MAX / B) return TBQ4_ERR_SHAPE;
+    if (ws_bytes < tree_ws_bytes(rows)) return TBQ4_ERR_WORKSPACE;
+    tree::TreeParams p = {};
+    p.q = q;
+    p.q_type = q_dtype;
+    p.k = k;
+    p.v = v;
+    p.capacity = capacity;
+    p.head_stride = capacity * kBlockBytes;
+    p.seq_stride = (int64_t)Hkv * p.head_stride;
+    p.cache_bytes = (int64_t)B * p.seq_stride;
+    if (pg) {
+        p.table = pg->block_table;
+        p.max_pages = pg->max_pages;
+        p.page_size = pg->page_size;
+        p.n_pages = pg->n_pages;
+        p.cache_bytes = pg->n_pages * pg->page_size * Hkv * kBlockBytes;
+    }
+    p.ctx_lens = ctx_lens;
+    p.n_nodes = n_nodes;
+    p.mask = reinterpret_cast<const unsigned long long *>(mask);
+    p.mask_stride = mask_stride;
+    p.B = B;
+    p.T = T;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.G = Hq / Hkv;
+    p.rows = rows;
+    p.scale = softmax_scale;
+    sign_words(sign_seed, &p.sign_lo, &p.sign_hi);
+    p.n_ctas = kNumSMs;
+    p.part_o = static_cast<float *>(workspace);
+    p.part_ml = reinterpret_cast<float2 *>(p.part_o + (size_t)2 * p.n_ctas * rows * kD);
+    p.out = out;
+    p.out_type = out_dtype;
+    p.out_elems = (int64_t)B * T * Hq * kD;
+    static bool attr_set[64] = {};
+    if (!ensure_smem_attr((const void *)tree::tree_plain_kernel, tree::kPlainSmem, attr_set))
+        return TBQ4_ERR_LAUNCH;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (g_ev_before) cudaEventRecord(g_ev_before, st);
+    tree::tree_plain_kernel<<<p.n_ctas, tree::kPlainWarps * 32, tree::kPlainSmem, st>>>(p);
+    // the join, a programmatic dependent launch: one CTA per start of a share
+    // and group of rows
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.n_ctas - 1,
+                       (unsigned)ceil_div(std::min(rows, T * p.G), tree::kJoinRows));
+    cfg.blockDim = dim3(tree::kJoinWarps * tree::kJoinRows * 32);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, tree::tree_combine_kernel, p) != cudaSuccess)
+        return TBQ4_ERR_LAUNCH;
+    if (g_ev_after) cudaEventRecord(g_ev_after, st);
+    return launch_status();
+}
+
+tbq4_status accept_impl(uint8_t *const *k_caches, uint8_t *const *v_caches, int n_layers,
+                        const int32_t *ctx_lens, const int32_t *path, const int32_t *n_accept,
+                        int max_path, int B, int Hkv, int64_t capacity, const PagedArgs *pg,
+                        int32_t *new_lens, void *stream) {
+    const NvtxRange range(pg ? "tbq4_tree_accept_paged" : "tbq4_tree_accept");
+    if (!k_caches || !v_caches || !ctx_lens || !path || !n_accept) return TBQ4_ERR_NULL;
+    if (pg) {
+        const tbq4_status e = check_paged(*pg, &capacity);
+        if (e != TBQ4_OK) return e;
+    }
+    if (!aligned(ctx_lens, 4) || !aligned(path, 4) || !aligned(n_accept, 4) ||
+        !aligned(new_lens, 4))
+        return TBQ4_ERR_ALIGN;
+    if (n_layers <= 0 || n_layers > kMaxAcceptLayers || B <= 0 || Hkv <= 0 || max_path <= 0 ||
+        max_path > kMaxPath || new_lens == ctx_lens)
+        return TBQ4_ERR_SHAPE;
+    if (capacity <= 0 || capacity % 8 != 0) return TBQ4_ERR_CAPACITY;
+    const int per = std::min(n_layers, kAcceptLayers);
+    if ((int64_t)2 * per * B * Hkv > (int64_t)kAcceptWarps * INT32_MAX) return TBQ4_ERR_SHAPE;
+    const uint8_t *all[2 * kMaxAcceptLayers];
+    for (int i = 0; i < n_layers; ++i) {
+        all[2 * i] = k_caches[i];
+        all[2 * i + 1] = v_caches[i];
+    }
+    for (int i = 0; i < 2 * n_layers; ++i) {
+        if (!all[i]) return TBQ4_ERR_NULL;
+        if (!aligned(all[i], 16)) return TBQ4_ERR_ALIGN;
+    }
+    std::sort(all, all + 2 * n_layers, std::less<const uint8_t *>());
+    if (std::adjacent_find(all, all + 2 * n_layers) != all + 2 * n_layers) return TBQ4_ERR_SHAPE;
+    AcceptParams p = {};
+    p.B = B;
+    p.Hkv = Hkv;
+    p.max_path = max_path;
+    p.capacity = capacity;
+    p.ctx_lens = ctx_lens;
+    p.path = path;
+    p.n_accept = n_accept;
+    p.cache_bytes = (int64_t)B * capacity * Hkv * kBlockBytes;
+    if (pg) {
+        p.table = pg->block_table;
+        p.max_pages = pg->max_pages;
+        p.page_size = pg->page_size;
+        p.n_pages = pg->n_pages;
+        p.cache_bytes = pg->n_pages * pg->page_size * Hkv * kBlockBytes;
+    }
+    for (int l0 = 0; l0 < n_layers; l0 += kAcceptLayers) {
+        const int n = std::min(kAcceptLayers, n_layers - l0);
+        for (int i = 0; i < n; ++i) {
+            p.cache[2 * i] = k_caches[l0 + i];
+            p.cache[2 * i + 1] = v_caches[l0 + i];
+        }
+        p.n_caches = 2 * n;
+        p.new_lens = l0 == 0 ? new_lens : nullptr;
+        const int64_t items = (int64_t)p.n_caches * B * Hkv;
+        tree_accept_kernel<<<(unsigned)ceil_div(items, kAcceptWarps), kAcceptWarps * 32, 0,
+                             (cudaStream_t)stream>>>(p);
+    }
+    return launch_status();
+}
+
+}  // namespace
+
+extern "C" {
+
+tbq4_status tbq4_rope_append(const void *q, int64_t q_token_stride, int64_t q_head_stride,
+                             const void *k, int64_t k_token_stride, int64_t k_head_stride,
+                             const void *v, int64_t v_token_stride, int64_t v_head_stride, int dtype,
+                             int n_tokens, int B, int Hq, int Hkv, const int32_t *seq_ids,
+                             const int32_t *slots, const int32_t *positions, const double *inv_freq,
+                             int rot_dim, int interleaved, int64_t capacity, uint64_t sign_seed,
+                             uint8_t *k_cache, uint8_t *v_cache, void *q_out, void *stream) {
+    return rope_impl({q, q_token_stride, q_head_stride}, {k, k_token_stride, k_head_stride},
+                     {v, v_token_stride, v_head_stride}, dtype, n_tokens, B, Hq, Hkv, seq_ids, slots,
+                     positions, inv_freq, rot_dim, interleaved, capacity, nullptr, sign_seed,
+                     k_cache, v_cache, q_out, stream);
+}
+
+tbq4_status tbq4_rope_append_paged(
+    const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *k,
+    int64_t k_token_stride, int64_t k_head_stride, const void *v, int64_t v_token_stride,
+    int64_t v_head_stride, int dtype, int n_tokens, int B, int Hq, int Hkv, const int32_t *seq_ids,
+    const int32_t *slots, const int32_t *positions, const double *inv_freq, int rot_dim,
+    int interleaved, const int32_t *block_table, int max_pages, int page_size, int64_t n_pages,
+    uint64_t sign_seed, uint8_t *k_pool, uint8_t *v_pool, void *q_out, void *stream) {
+    const PagedArgs pg = {block_table, max_pages, page_size, n_pages};
+    return rope_impl({q, q_token_stride, q_head_stride}, {k, k_token_stride, k_head_stride},
+                     {v, v_token_stride, v_head_stride}, dtype, n_tokens, B, Hq, Hkv, seq_ids, slots,
+                     positions, inv_freq, rot_dim, interleaved, 0, &pg, sign_seed, k_pool, v_pool,
+                     q_out, stream);
+}
+
+size_t tbq4_tree_workspace_bytes(int B, int T, int Hq, int Hkv) {
+    if (B <= 0 || B > tree::kMaxBatch || T <= 0 || T > tree::kMaxNodes || Hkv <= 0 || Hq <= 0 ||
+        Hq % Hkv != 0 || Hq / Hkv > kMaxGroup)
+        return 0;
+    return tree_ws_bytes(tree_rows(TBQ4_BF16));
+}
+
+tbq4_status tbq4_attn_tree(const void *q, int q_dtype, const uint8_t *k_cache,
+                           const uint8_t *v_cache, const int32_t *ctx_lens, const int32_t *n_nodes,
+                           const uint64_t *tree_mask, int64_t mask_stride, int B, int T, int Hq,
+                           int Hkv, int64_t capacity, float softmax_scale, uint64_t sign_seed,
+                           void *workspace, size_t ws_bytes, void *out, int out_dtype,
+                           void *stream) {
+    return tree_impl(q, q_dtype, k_cache, v_cache, ctx_lens, n_nodes, tree_mask, mask_stride, B, T,
+                     Hq, Hkv, capacity, nullptr, softmax_scale, sign_seed, workspace, ws_bytes, out,
+                     out_dtype, stream);
+}
+
+tbq4_status tbq4_attn_tree_paged(const void *q, int q_dtype, const uint8_t *k_pool,
+                                 const uint8_t *v_pool, const int32_t *block_table, int max_pages,
+                                 int page_size, int64_t n_pages, const int32_t *ctx_lens,
+                                 const int32_t *n_nodes, const uint64_t *tree_mask,
+                                 int64_t mask_stride, int B, int T, int Hq, int Hkv,
+                                 float softmax_scale, uint64_t sign_seed, void *workspace,
+                                 size_t ws_bytes, void *out, int out_dtype, void *stream) {
+    const PagedArgs pg = {block_table, max_pages, page_size, n_pages};
+    return tree_impl(q, q_dtype, k_pool, v_pool, ctx_lens, n_nodes, tree_mask, mask_stride, B, T,
+                     Hq, Hkv, 0, &pg, softmax_scale, sign_seed, workspace, ws_bytes, out, out_dtype,
+                     stream);
+}
+
+tbq4_status tbq4_tree_accept(uint8_t *const *k_caches, uint8_t *const *v_caches, int n_layers,
+                             const int32_t *ctx_lens, const int32_t *path, const int32_t *n_accept,
+                             int max_path, int B, int Hkv, int64_t capacity, int32_t *new_lens,
+                             void *stream) {
+    return accept_impl(k_caches, v_caches, n_layers, ctx_lens, path, n_accept, max_path, B, Hkv,
+                       capacity, nullptr, new_lens, stream);
+}
+
+tbq4_status tbq4_tree_accept_paged(uint8_t *const *k_pools, uint8_t *const *v_pools, int n_layers,
+                                   const int32_t *block_table, int max_pages, int page_size,
+                                   int64_t n_pages, const int32_t *ctx_lens, const int32_t *path,
+                                   const int32_t *n_accept, int max_path, int B, int Hkv,
+                                   int32_t *new_lens, void *stream) {
+    const PagedArgs pg = {block_table, max_pages, page_size, n_pages};
+    return accept_impl(k_pools, v_pools, n_layers, ctx_lens, path, n_accept, max_path, B, Hkv, 0,
+                       &pg, new_lens, stream);
 }
 
 void tbq4_set_timing_events(void *before, void *after) {
