@@ -257,105 +257,5 @@ __device__ __forceinline__ int64_t piece_offset(const TreeParams &p, int b, int 
     return (((int64_t)pid * p.Hkv + g) * p.page_size + t % p.page_size) * kBlockBytes;
 }
 
-// Plain kernel: 32 tokens at a time dequantised into shared memory, fp32
-// products on the CUDA cores.  A warp owns four of the block's rows: lane =
-// token for the scores, lane = four dimensions for the output.
-constexpr int kPlainRows = 32, kPlainWarps = 8;
-constexpr int kPlainSmem = (3 * 32 * (kD + 1)) * 4;
-
-__global__ void __launch_bounds__(kPlainWarps * 32)
-tree_plain_kernel(const TreeParams p) {
-    extern __shared__ float sm[];
-    __shared__ int prefix[kMaxBatch + 1];
-    float *qs = sm, *ks = sm + 32 * (kD + 1), *vs = ks + 32 * (kD + 1);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    build_prefix(p, prefix);
-    const int units = prefix[p.B], shares = n_shares(p, units), cta = blockIdx.x;
-    if (cta >= shares) return;
-    int u = share_begin(units, cta, shares);
-    const int end = share_begin(units, cta + 1, shares);
-    const uint32_t sbits = lane_sign_bits(p.sign_lo, p.sign_hi, lane);
-    const float c = p.scale * 1.4426950408889634f;
-    while (u < end) {
-        const Segment s = segment_at(p, prefix, u, end);
-        u += s.tiles;
-        __syncthreads();
-        for (int r = warp; r < 32; r += kPlainWarps) {
-            float v[4] = {0.f, 0.f, 0.f, 0.f};
-            if (r < s.rows) {
-                const int row = s.row0 + r, i = row / p.G, h = s.g * p.G + row % p.G;
-                load4(p.q, p.q_type, (((int64_t)s.b * p.T + i) * p.Hq + h) * kD + 4 * lane, v);
-                warp_rotate128(v, sbits, lane);
-            }
-            for (int k = 0; k < 4; ++k) qs[r * (kD + 1) + 4 * lane + k] = v[k] * c;
-        }
-        float m[4], l[4];
-        float o[4][4] = {};
-        unsigned long long mask[4];
-        for (int k = 0; k < 4; ++k) {
-            const int row = s.row0 + 4 * warp + k;
-            m[k] = -INFINITY;
-            l[k] = 0.f;
-            mask[k] = 4 * warp + k < s.rows ? p.mask[s.b * p.mask_stride + row / p.G] : 0ull;
-        }
-        const int stop = min((s.tile0 + s.tiles) * kTileT, s.ctx + s.n);
-        for (int t0 = s.tile0 * kTileT; t0 < stop; t0 += 32) {
-            __syncthreads();
-            const int64_t off = piece_offset(p, s.b, s.g, t0);
-            for (int e = threadIdx.x; e < 2 * 32 * 64; e += blockDim.x) {
-                const int which = e >> 11, t = (e >> 6) & 31, j = e & 63;
-                float *dst = (which ? vs : ks) + t * (kD + 1) + 2 * j;
-                float lo = 0.f, hi = 0.f;
-                const int64_t o1 = off + (int64_t)t * kBlockBytes;
-                if (t0 + t < stop && in_extent(o1, kBlockBytes, p.cache_bytes)) {
-                    const uint8_t *blk = (which ? p.v : p.k) + o1;
-                    const float S = half_bits_to_float(*reinterpret_cast<const uint16_t *>(blk)) / 15.0f;
-                    const int x = blk[2 + j];
-                    lo = S * (float)(2 * (x & 15) - 15);
-                    hi = S * (float)(2 * (x >> 4) - 15);
-                }
-                dst[0] = lo;
-                dst[1] = hi;
-            }
-            __syncthreads();
-            const int t = t0 + lane, j = t - s.ctx;
-            for (int k = 0; k < 4; ++k) {
-                const float *qr = qs + (4 * warp + k) * (kD + 1);
-                float x = 0.f;
-                for (int d = 0; d < kD; ++d) x = fmaf(qr[d], ks[lane * (kD + 1) + d], x);
-                const bool sees = t < stop && (j < 0 || ((mask[k] >> j) & 1ull));
-                if (!sees) x = -INFINITY;
-                const float mn = fmaxf(m[k], warp_max(x));
-                const float a = mn == -INFINITY ? 1.f : exp2f(m[k] - mn);
-                const float pr = sees ? exp2f(x - mn) : 0.f;
-                m[k] = mn;
-                l[k] = l[k] * a + warp_sum(pr);
-                for (int e = 0; e < 4; ++e) o[k][e] *= a;
-                for (int tt = 0; tt < 32; ++tt) {
-                    const float w = __shfl_sync(kFull, pr, tt);
-                    if (w == 0.f) continue;                  // a hidden token adds nothing, whatever it holds
-                    for (int e = 0; e < 4; ++e)
-                        o[k][e] = fmaf(w, vs[tt * (kD + 1) + 4 * lane + e], o[k][e]);
-                }
-            }
-        }
-        for (int k = 0; k < 4; ++k) {
-            const int r = 4 * warp + k;
-            if (r >= s.rows) continue;
-            if (s.tiles == s.work_tiles) {
-                const float inv = l[k] == 0.f ? 0.f : 1.0f / l[k];
-                float v[4] = {o[k][0] * inv, o[k][1] * inv, o[k][2] * inv, o[k][3] * inv};
-                store_out(p, s.b, s.g, s.row0 + r, v, lane);
-            } else {
-                const int64_t row = (int64_t)part_slot(s, cta) * p.rows + r;
-                reinterpret_cast<float4 *>(p.part_o + row * kD)[lane] =
-                    make_float4(o[k][0], o[k][1], o[k][2], o[k][3]);
-                if (lane == 0) p.part_ml[row] = make_float2(m[k], l[k]);
-            }
-        }
-    }
-}
-
 }  // namespace tree
 }  // namespace tbq4

@@ -1,0 +1,770 @@
+// decode_tree_tc.cuh -- tree attention over TBQ4 caches on the tensor cores
+// (tcgen05); the operator, its work schedule and its join are in
+// decode_tree.cuh.
+//
+// Per tile of 128 tokens and a block of N query rows (N <= 128):
+//
+//   S^T (128 tokens x N) = K (128 x 128, fp16 levels, tensor memory) . Q^T
+//   O^T (128 dims x N)  += V^T (128 dims x 128 tokens, fp16 levels) . P'^T
+//
+// Tokens are the rows of S^T and dimensions the rows of O^T, so the width of
+// both products is the number of query rows: a small tree pays for its own
+// rows only.  Operands:
+//   K, V  levels (2n - 15) 2^-11, exact in fp16 (nibbles masked into
+//         subnormals, one HFMA2); the block scales stay out of the products.
+//         A word of nibbles gives eight levels in the order 0 4 1 5 2 6 3 7,
+//         which is the order of the dimensions in every operand here.  K goes
+//         from registers to tensor memory, thread = token = lane; V goes to
+//         shared memory as it lies, token by token, and enters as the
+//         MN-major operand (no transposition anywhere).
+//   Q     q_rot times a power of two that brings the block's largest finite
+//         channel below 2^15: 28 binades of rows below the largest keep all
+//         11 bits.  kTerms = 2 adds the remainder as a second fp16 term.
+//   P'    p S_v ps, thread = token writes eight rows per 16-byte store
+//         (MN-major).  ps is the power of two that keeps S_v ps <= 2^7 for
+//         every V scale seen so far (p <= 2^8): most weights stay normal fp16
+//         numbers.  When it shrinks, O moves with it.  kTerms = 2 adds the
+//         remainder as a second term.
+// One term rounds a query or a weight by up to 2^-11 relative, a tenth of a
+// bf16 output's own rounding; fp16 outputs, which that would double, take two
+// terms (22 bits) and blocks of 64 rows in the same shared memory.
+//
+// Softmax.  thread = token, so its S_k and S_v are scalars and a row's
+// running maximum is one number for all threads (shared memory).  The
+// maximum moves only when a logit exceeds it by 2^3 in log2 units: one
+// barrier-with-vote per tile decides that, and the rare path takes the tile's
+// maxima and rescales O.  Sums stay in registers until the end.  Tiles that
+// hold drafted nodes or the end of the sequence apply masks by select, to
+// logits and to weights (a hidden block may hold anything).
+//
+// Warps (28): 0 producer (cp.async.bulk, 32-token pieces), 1 tensor-memory
+// allocation and every tcgen05.mma, 4-7 K levels, 8-11 V levels, 12-27
+// softmax (four warpgroups; 8-row chunk c belongs to warpgroup c % 4).
+// Hand-offs are mbarriers with bounded waits; a warp whose wait runs out
+// records the error and goes on without waiting, so the named barriers of
+// its warpgroup and of the CTA always fill.
+#pragma once
+#include "decode_tree.cuh"
+#include "tcgen05.cuh"
+
+namespace tbq4 {
+namespace tree {
+
+constexpr int kTcThreads = 896;
+constexpr int kSoftWarp0 = 12, kSoftWarps = 16;
+constexpr int kRaw = 3;                                 // raw tiles in flight, K and V each
+constexpr int kRawTile = kTileT * kBlockBytes;          // 8448
+constexpr int kRawStride = kRawTile + 16;
+constexpr uint32_t kSpinTree = 1u << 22;
+constexpr float kGrow = 8.0f;                           // log2 units
+constexpr float kLowest = -1e30f;                       // running maximum before any token
+// registers per thread by warpgroup: control, levels (2), softmax (4)
+// (setmaxnreg draws on what the block was launched with: the host refuses to
+// launch a build that compiled to fewer than kLaunchRegs)
+constexpr uint32_t kRegCtl = 24, kRegLev = 48, kRegSoft = 96;
+constexpr int kLaunchRegs = 72;
+static_assert(4 * kRegCtl + 8 * kRegLev + 16 * kRegSoft <= 28 * kLaunchRegs, "register split");
+
+constexpr int kOffQ = 0;                                // 32 KB: kTerms x rows x 256 B
+constexpr int kOffP = 32768;                            // 2 x 32 KB: kTerms x rows/64 x 16 KB
+constexpr int kOffV = kOffP + 2 * 32768;                // 2 x 32 KB
+constexpr int kOffRawK = kOffV + 2 * 32768;
+constexpr int kOffRawV = kOffRawK + kRaw * kRawStride;
+constexpr int kOffSig = kOffRawV + kRaw * kRawStride;   // S_k, S_v ps: [2][2][128] floats
+constexpr int kOffNegM = kOffSig + 2 * 2 * kTileT * 4;  // minus the running maxima [128]
+constexpr int kOffXch = kOffNegM + 128 * 4;             // [4][128] floats
+constexpr int kOffLinv = kOffXch + 4 * 128 * 4;         // [128] floats
+constexpr int kOffVis = kOffLinv + 128 * 4;             // [64 nodes][4] words: rows that see it
+constexpr int kOffPs = kOffVis + kMaxNodes * 16;        // [2] x (factor, ps)
+constexpr int kOffMax = kOffPs + 16;                    // [2][4] floats: V scales
+constexpr int kOffQMax = kOffMax + 32;                  // bits of the largest |q_rot|
+constexpr int kOffTmem = kOffQMax + 8;
+constexpr int kOffBars = kOffTmem + 8;
+constexpr int kTreeBars = 4 * kRaw + 12 + 1;
+constexpr int kOffPrefix = kOffBars + kTreeBars * 8;
+constexpr int kTcSmem = kOffPrefix + (kMaxBatch + 1) * 4 + 1024;   // + alignment slack
+static_assert(kOffRawK % 16 == 0 && kRawStride % 16 == 0 && kOffBars % 8 == 0 && kOffVis % 16 == 0,
+              "alignment");
+static_assert(kTcSmem <= 232448, "shared memory");
+
+// tensor memory columns: S (two buffers of 128), O, K levels (two of 64)
+constexpr uint32_t kColS = 0, kColO = 256, kColK = 384;
+
+__device__ __forceinline__ void named_sync(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ bool named_or(int id, int threads, bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %3, 0;\n bar.red.or.pred q, %1, %2, p;\n"
+        " selp.u32 %0, 1, 0, q;\n}\n"
+        : "=r"(r)
+        : "r"(id), "r"(threads), "r"((uint32_t)x)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ float warp_redux_max(float x) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// two binary32 operations per instruction
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t half2_bits(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Eight levels (2n - 15) 2^-11 of a word of nibbles, as four fp16 pairs: the
+// nibbles 0 4 1 5 2 6 3 7 (dmq::vlo, dmq::vhi).
+__device__ __forceinline__ void word_levels(uint32_t w, uint32_t (&o)[4]) {
+    o[0] = dmq::vlo(w);
+    o[1] = dmq::vhi(w);
+    o[2] = dmq::vlo(w >> 8);
+    o[3] = dmq::vhi(w >> 8);
+}
+// Dimension at position `pos` of an operand: the order above, by eights.
+__device__ __forceinline__ int dim_at(int pos) {
+    return (pos & ~7) | ((pos & 1) << 2) | ((pos & 7) >> 1);
+}
+
+// Sum over the warp of 32 values per lane: lane l gets the sum of v[l].
+__device__ __forceinline__ float transpose_sum(float (&v)[32], int lane) {
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) {
+        const bool up = (lane & m) != 0;
+#pragma unroll
+        for (int k = 0; k < m; ++k) {
+            const float give = up ? v[k] : v[k + m], keep = up ? v[k + m] : v[k];
+            v[k] = keep + __shfl_xor_sync(kFull, give, m);
+        }
+    }
+    return v[0];
+}
+
+template <int kTerms>
+__global__ void __launch_bounds__(kTcThreads, 1)
+tree_tc_kernel(const __grid_constant__ TreeParams p) {
+    constexpr int kRows = 128 / kTerms;                 // rows per block, at most
+    constexpr int kChunks = kRows / 32;                 // 8-row chunks per warpgroup, at most
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    const uint32_t sbase = smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    int *prefix = reinterpret_cast<int *>(smem + kOffPrefix);
+    build_prefix(p, prefix);
+    const int units = prefix[p.B], shares = n_shares(p, units), cta = blockIdx.x;
+    if (cta >= shares) return;
+    const int u0 = share_begin(units, cta, shares), u1 = share_begin(units, cta + 1, shares);
+
+    const uint32_t bar0 = sbase + kOffBars;
+    auto kraw_full = [&](int s) { return bar0 + 8 * s; };
+    auto kraw_empty = [&](int s) { return bar0 + 8 * (kRaw + s); };
+    auto vraw_full = [&](int s) { return bar0 + 8 * (2 * kRaw + s); };
+    auto vraw_empty = [&](int s) { return bar0 + 8 * (3 * kRaw + s); };
+    const uint32_t bx = bar0 + 8 * 4 * kRaw;
+    auto k_full = [&](int b) { return bx + 8 * b; };            // K levels -> MMA
+    auto s_full = [&](int b) { return bx + 8 * (2 + b); };      // S ready (K levels read)
+    auto s_empty = [&](int b) { return bx + 8 * (4 + b); };     // S and S_k read
+    auto v_full = [&](int b) { return bx + 8 * (6 + b); };      // V levels -> MMA
+    auto p_full = [&](int b) { return bx + 8 * (8 + b); };      // P' -> MMA
+    auto pv_done = [&](int b) { return bx + 8 * (10 + b); };    // V levels and P' read
+    const uint32_t drained = bx + 8 * 12;
+    uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(smem + kOffTmem);
+    float *sig_k = reinterpret_cast<float *>(smem + kOffSig);       // [2][128]
+    float *sig_v = sig_k + 2 * kTileT;                              // [2][128]
+    float *negm = reinterpret_cast<float *>(smem + kOffNegM);
+    float *xch = reinterpret_cast<float *>(smem + kOffXch);
+    float *linv = reinterpret_cast<float *>(smem + kOffLinv);
+    uint32_t *vis = reinterpret_cast<uint32_t *>(smem + kOffVis);
+    float *tps = reinterpret_cast<float *>(smem + kOffPs);
+    float *vmax = reinterpret_cast<float *>(smem + kOffMax);
+    uint32_t *qmax = reinterpret_cast<uint32_t *>(smem + kOffQMax);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kRaw; ++s) {
+            mbar_init(kraw_full(s), 1);
+            mbar_init(kraw_empty(s), 4);
+            mbar_init(vraw_full(s), 1);
+            mbar_init(vraw_empty(s), 4);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(k_full(b), 4);
+            mbar_init(s_full(b), 1);
+            mbar_init(s_empty(b), kSoftWarps);
+            mbar_init(v_full(b), 4);
+            mbar_init(p_full(b), kSoftWarps);
+            mbar_init(pv_done(b), 1);
+        }
+        mbar_init(drained, 1);
+        *qmax = 0u;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tc::tmem_alloc(smem_u32(tmem_ptr), 512);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = *tmem_ptr;
+
+    bool ok = true;                                     // this warp's waits have all come through
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (ok && !mbar_wait_bounded(bar, parity, kSpinTree)) {
+            ok = false;
+            record_status(7u /* TBQ4_ERR_DEVICE_TIMEOUT */);
+        }
+    };
+    // everyone but the producer and the two idle warps, at the start of a
+    // segment (twice) and at its end
+    auto all_sync = [&]() { named_sync(1, 25 * 32); };
+
+    if (warp < 4) {
+        tc::regs_dec<kRegCtl>();
+        if (warp == 0) {
+            // ======================= producer ================================
+            int it = 0;
+            for (int u = u0; u < u1 && ok;) {
+                const Segment s = segment_at(p, prefix, u, u1);
+                u += s.tiles;
+                const int stop = s.ctx + s.n;
+                for (int j = 0; j < s.tiles; ++j, ++it) {
+                    const int st = it % kRaw;
+                    if (it >= kRaw) {
+                        wait(kraw_empty(st), ((it / kRaw) - 1) & 1);
+                        wait(vraw_empty(st), ((it / kRaw) - 1) & 1);
+                        if (!ok) break;
+                    }
+                    const int t = (s.tile0 + j) * kTileT;
+                    // whole 8-row groups: capacity and page size are multiples of 8
+                    const int rows = (min(kTileT, stop - t) + 7) & ~7;
+                    if (lane == 0) {
+                        fence_proxy_async();
+                        mbar_expect_tx(kraw_full(st), (uint32_t)rows * kBlockBytes);
+                        mbar_expect_tx(vraw_full(st), (uint32_t)rows * kBlockBytes);
+                    }
+                    __syncwarp();
+                    const int r0 = (lane >> 1) * 32;
+                    if (lane < 8 && r0 < rows) {
+                        const uint32_t nb = (uint32_t)min(32, rows - r0) * kBlockBytes;
+                        int64_t off = piece_offset(p, s.b, s.g, t + r0);
+                        if constexpr (kDebugBounds) off = checked_off(off, nb, p.cache_bytes);
+                        const uint32_t to = sbase + st * kRawStride + r0 * kBlockBytes;
+                        if (lane & 1)
+                            bulk_g2s(to + kOffRawV, p.v + off, nb, vraw_full(st));
+                        else
+                            bulk_g2s(to + kOffRawK, p.k + off, nb, kraw_full(st));
+                    }
+                }
+            }
+            // after a lost hand-off: the copies still in flight land before the
+            // shared memory goes away
+            for (int i = max(0, it - kRaw); i < it; ++i) {
+                mbar_wait_bounded(kraw_full(i % kRaw), (i / kRaw) & 1, kSpinTree);
+                mbar_wait_bounded(vraw_full(i % kRaw), (i / kRaw) & 1, kSpinTree);
+            }
+        } else if (warp == 1) {
+            // ======================= MMA issuer ==============================
+            int it0 = 0;
+            for (int u = u0; u < u1;) {
+                const Segment s = segment_at(p, prefix, u, u1);
+                u += s.tiles;
+                const int N = (s.rows + 15) & ~15;
+                const uint32_t idesc_qk = tc::idesc_f16(128, N, false);
+                const uint32_t idesc_pv = tc::idesc_f16(128, N, true);
+                all_sync();
+                all_sync();
+                tc::fence_after_sync();
+                if (lane == 0) {
+                    int jq = 0, jp = 0;                 // next QK and PV of this segment
+                    uint32_t idle = 0;
+                    while (ok && jp < s.tiles) {
+                        bool moved = false;
+                        if (jq < s.tiles && jq <= jp + 1) {
+                            const int it = it0 + jq, b = it & 1;
+                            if (mbar_test(k_full(b), (it >> 1) & 1) &&
+                                (it < 2 || mbar_test(s_empty(b), ((it >> 1) - 1) & 1))) {
+                                tc::fence_after_sync();
+#pragma unroll
+                                for (int i = 0; i < 8 * kTerms; ++i) {
+                                    const int ki = i & 7;
+                                    tc::mma_ts(tmem + kColS + 128 * b, tmem + kColK + 64 * b + 8 * ki,
+                                               tc::desc_sw128(sbase + kOffQ + (i >> 3) * (kRows * 256) +
+                                                              (ki >> 2) * (kRows * 128) + (ki & 3) * 32),
+                                               idesc_qk, i > 0);
+                                }
+                                tc::mma_commit(s_full(b));
+                                ++jq;
+                                moved = true;
+                            }
+                        }
+                        if (jp < jq) {
+                            const int it = it0 + jp, b = it & 1;
+                            if (mbar_test(p_full(b), (it >> 1) & 1) &&
+                                mbar_test(v_full(b), (it >> 1) & 1)) {
+                                tc::fence_after_sync();
+                                const uint32_t vt = sbase + kOffV + 32768 * b;
+                                const uint32_t pt = sbase + kOffP + 32768 * b;
+#pragma unroll
+                                for (int i = 0; i < 8 * kTerms; ++i)
+                                    tc::mma_ss(tmem + kColO,
+                                               tc::desc_mn_sw128(vt + 2048 * (i & 7), 16384),
+                                               tc::desc_mn_sw128(pt + (i >> 3) * 16384 + 2048 * (i & 7),
+                                                                 16384),
+                                               idesc_pv, (jp > 0 || i > 0) ? 1u : 0u);
+                                tc::mma_commit(pv_done(b));
+                                ++jp;
+                                moved = true;
+                            }
+                        }
+                        if (moved) {
+                            idle = 0;
+                        } else {
+                            __nanosleep(20);
+                            if (++idle > kSpinTree) {
+                                ok = false;
+                                record_status(7u);
+                            }
+                        }
+                    }
+                }
+                __syncwarp();
+                it0 += s.tiles;
+                all_sync();
+            }
+            if (lane == 0) {                            // every product issued has ended
+                tc::mma_commit(drained);
+                mbar_wait_thread(drained, 0, kSpinTree);
+            }
+            __syncwarp();
+            tc::fence_after_sync();
+            tc::tmem_dealloc(tmem, 512);
+        }
+    } else if (warp < 8) {
+        // ======================= K levels ====================================
+        tc::regs_dec<kRegLev>();
+        const int t = threadIdx.x - 4 * 32;             // token of the tile = tensor-memory lane
+        const uint32_t t_lane = tmem + ((uint32_t)(t & ~31) << 16);
+        int it = 0;
+        for (int u = u0; u < u1;) {
+            const Segment s = segment_at(p, prefix, u, u1);
+            u += s.tiles;
+            // rows of the block that see node j, one bit each (word w: rows 32 w ..)
+            for (int e = t; e < kMaxNodes * 4; e += 128) {
+                const int j = e >> 2, c0 = s.row0 + 32 * (e & 3);
+                uint32_t bits = 0;
+                if (j < s.n) {
+                    int i = c0 / p.G, h = c0 - i * p.G;
+                    for (int k = 0; k < 32 && i < s.n; ++k) {
+                        bits |= (uint32_t)((__ldg(p.mask + s.b * p.mask_stride + i) >> j) & 1ull) << k;
+                        if (++h == p.G) { h = 0; ++i; }
+                    }
+                }
+                vis[e] = bits;
+            }
+            all_sync();
+            all_sync();
+            for (int j = 0; j < s.tiles; ++j, ++it) {
+                const int st = it % kRaw, b = it & 1;
+                wait(kraw_full(st), (it / kRaw) & 1);
+                // the softmax has read S and S_k of tile it - 2, so its product
+                // is done with this K buffer
+                if (it >= 2) wait(s_empty(b), ((it >> 1) - 1) & 1);
+                tc::fence_after_sync();
+                const uint32_t row = sbase + kOffRawK + st * kRawStride + t * kBlockBytes;
+                sig_k[kTileT * b + t] = half_bits_to_float((uint16_t)dmq::lds16(row));
+                const uint32_t a0 = (row + 2) & ~3u, sh = ((row + 2) & 3u) * 8u;
+                uint32_t w = dmq::lds32(a0);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {           // four words: 32 levels, 16 columns
+                    uint32_t o[16];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t nx = dmq::lds32(a0 + 4 * (4 * c + i + 1));
+                        uint32_t l[4];
+                        word_levels(__funnelshift_r(w, nx, sh), l);
+                        w = nx;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[4 * i + e] = l[e];
+                    }
+                    tc::tmem_st16(t_lane + kColK + 64 * b + 16 * c, o);
+                }
+                tc::tmem_wait_st();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(k_full(b));
+                    mbar_arrive(kraw_empty(st));
+                }
+            }
+            all_sync();
+        }
+    } else if (warp < kSoftWarp0) {
+        // ======================= V levels ====================================
+        tc::regs_dec<kRegLev>();
+        const int t = threadIdx.x - 8 * 32;             // token of the tile
+        int it = 0;
+        for (int u = u0; u < u1;) {
+            const Segment s = segment_at(p, prefix, u, u1);
+            u += s.tiles;
+            const int stop = s.ctx + s.n;
+            float ps = 0.f;                             // 0 until a nonzero scale arrives
+            all_sync();
+            all_sync();
+            for (int j = 0; j < s.tiles; ++j, ++it) {
+                const int st = it % kRaw, b = it & 1;
+                wait(vraw_full(st), (it / kRaw) & 1);
+                if (it >= 2) wait(pv_done(b), ((it >> 1) - 1) & 1);
+                const uint32_t row = sbase + kOffRawV + st * kRawStride + t * kBlockBytes;
+                const float sv = (s.tile0 + j) * kTileT + t < stop
+                    ? half_bits_to_float((uint16_t)dmq::lds16(row)) : 0.f;
+                // the tile's largest finite scale
+                const float mine = warp_redux_max(isfinite(sv) ? sv : 0.f);
+                if (lane == 0) vmax[4 * b + (warp & 3)] = mine;
+                named_sync(2, 128);
+                const float4 m4 = *reinterpret_cast<const float4 *>(vmax + 4 * b);
+                const float top = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
+                float f = 1.f;
+                if (ps == 0.f ? top > 0.f : top * ps > 128.0f) {
+                    const float nps = pow2_floor(__fdividef(128.0f, top));
+                    f = ps == 0.f ? 1.f : pow2_ratio(nps, ps);
+                    ps = nps;
+                }
+                sig_v[kTileT * b + t] = sv * ps;
+                if (t == 0) {
+                    tps[2 * b] = f;
+                    tps[2 * b + 1] = ps;
+                }
+                const uint32_t a0 = (row + 2) & ~3u, sh = ((row + 2) & 3u) * 8u;
+                const uint32_t to = sbase + kOffV + 32768 * b + t * 128;
+                uint32_t w = dmq::lds32(a0);
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {          // a word: eight levels, 16 bytes
+                    const uint32_t nx = dmq::lds32(a0 + 4 * (c + 1));
+                    uint32_t l[4];
+                    word_levels(__funnelshift_r(w, nx, sh), l);
+                    w = nx;
+                    dmq::sts128(to + (c >> 3) * 16384 + (((c & 7) ^ (t & 7)) << 4), l[0], l[1], l[2], l[3]);
+                }
+                fence_proxy_async();                    // read by the tensor core
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(v_full(b));
+                    mbar_arrive(vraw_empty(st));
+                }
+            }
+            all_sync();
+        }
+    } else {
+        // ======================= softmax =====================================
+        tc::regs_inc<kRegSoft>();
+        const int ws = warp - kSoftWarp0, wg = ws >> 2, q4 = warp & 3;
+        const int t = 32 * q4 + lane;                   // token, at the end position of a dimension
+        const uint32_t t_lane = tmem + ((uint32_t)(32 * q4) << 16);
+        const uint32_t sbits = lane_sign_bits(p.sign_lo, p.sign_hi, lane);
+        const int wg_bar = 4 + wg;
+        int it = 0;
+        for (int u = u0; u < u1;) {
+            const Segment s = segment_at(p, prefix, u, u1);
+            const bool whole = s.tiles == s.work_tiles;
+            u += s.tiles;
+            const int N = (s.rows + 15) & ~15, nch = N >> 3;
+            // ---- queries: rotate, agree on the power of two, store -----------
+            float ql[kRows / kSoftWarps][4];
+            float mx = 0.f;
+#pragma unroll
+            for (int k = 0; k < kRows / kSoftWarps; ++k) {
+                const int r = ws + kSoftWarps * k;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) ql[k][e] = 0.f;
+                if (r < s.rows) {
+                    const int c = s.row0 + r, i = c / p.G, h = s.g * p.G + (c - i * p.G);
+                    load4(p.q, p.q_type, (((int64_t)s.b * p.T + i) * p.Hq + h) * kD + 4 * lane, ql[k]);
+                    warp_rotate128(ql[k], sbits, lane);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float a = fabsf(ql[k][e]);
+                        if (isfinite(a)) mx = fmaxf(mx, a);
+                    }
+                }
+            }
+            mx = warp_max(mx);
+            if (lane == 0 && mx > 0.f) atomicMax(qmax, __float_as_uint(mx));
+            if (ws * 8 < kRows && lane < 8) negm[ws * 8 + lane] = -kLowest;
+            all_sync();
+            const float big = __uint_as_float(*qmax);
+            int e2 = 0;
+            if (big > 0.f) frexpf(big, &e2);            // big < 2^e2
+            e2 = max(e2, -100);
+            const float up = ldexpf(1.0f, 15 - e2);
+            // log2 logit = S skc with skc = S_k c (levels are (2n - 15) 2^-11)
+            const float c2 = p.scale * (1.4426950408889634f * 2048.0f / 15.0f) * ldexpf(1.0f, e2 - 15);
+#pragma unroll
+            for (int k = 0; k < kRows / kSoftWarps; ++k) {
+                const int r = ws + kSoftWarps * k;
+                if (r >= N) continue;
+                // the operands' order of dimensions: pairs (d, d + 4) of each eight
+                const bool odd = lane & 1;
+                float x[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = ql[k][e] * up;
+                const float g0 = __shfl_xor_sync(kFull, odd ? x[0] : x[2], 1);
+                const float g1 = __shfl_xor_sync(kFull, odd ? x[1] : x[3], 1);
+                const float a0 = odd ? g0 : x[0], b0 = odd ? x[2] : g0;
+                const float a1 = odd ? g1 : x[1], b1 = odd ? x[3] : g1;
+                const int ch = lane >> 1;
+                const uint32_t at = sbase + kOffQ + (ch >> 3) * (kRows * 128) + (r >> 3) * 1024 +
+                                    (r & 7) * 128 + (((ch & 7) ^ (r & 7)) << 4) + (odd ? 8 : 0);
+                const __half2 h0 = __floats2half2_rn(a0, b0), h1 = __floats2half2_rn(a1, b1);
+                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at),
+                             "r"(*reinterpret_cast<const uint32_t *>(&h0)),
+                             "r"(*reinterpret_cast<const uint32_t *>(&h1)) : "memory");
+                if constexpr (kTerms == 2) {
+                    const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
+                    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + kRows * 256),
+                                 "r"(half2_bits(a0 - f0.x, b0 - f0.y)),
+                                 "r"(half2_bits(a1 - f1.x, b1 - f1.y)) : "memory");
+                }
+            }
+            fence_proxy_async();                        // read by the tensor core
+            all_sync();
+            if (ws == 0 && lane == 0) *qmax = 0u;       // for the next segment (read before the barrier)
+
+            float lp[8 * kChunks];
+#pragma unroll
+            for (int k = 0; k < 8 * kChunks; ++k) lp[k] = 0.f;
+            for (int j = 0; j < s.tiles; ++j, ++it) {
+                const int b = it & 1;
+                const uint32_t par = (it >> 1) & 1;
+                const int ta = (s.tile0 + j) * kTileT;
+                const bool masked = ta + kTileT > s.ctx;
+                wait(s_full(b), par);
+                wait(k_full(b), par);
+                wait(v_full(b), par);
+                tc::fence_after_sync();
+                if (wg >= nch) {                        // no rows for this warpgroup
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(s_empty(b));
+                        mbar_arrive(p_full(b));
+                    }
+                    continue;
+                }
+                const float skc = sig_k[kTileT * b + t] * c2, svp = sig_v[kTileT * b + t];
+                const float fsv = tps[2 * b];
+                const uint64_t sk2 = pack2(skc, skc), sv2 = pack2(svp, svp);
+                // the word of rows that see this token, for chunk c
+                auto rows_seeing = [&](int c) -> uint32_t {
+                    const int node = ta + t - s.ctx;
+                    const uint32_t w = node < 0 ? 0xFFFFFFFFu
+                                     : node < s.n ? vis[4 * node + (c >> 2)] : 0u;
+                    return w >> (8 * (c & 3));
+                };
+                float x[8 * kChunks];
+                float top = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < kChunks; ++i) {
+                    const int c = wg + 4 * i;
+                    if (c >= nch) break;
+                    uint32_t r[8];
+                    tc::tmem_ld8(t_lane + kColS + 128 * b + 8 * c, r);
+                    const float4 n0 = *reinterpret_cast<const float4 *>(negm + 8 * c);
+                    const float4 n1 = *reinterpret_cast<const float4 *>(negm + 8 * c + 4);
+                    tc::tmem_wait_ld();
+                    const float nm[8] = {n0.x, n0.y, n0.z, n0.w, n1.x, n1.y, n1.z, n1.w};
+#pragma unroll
+                    for (int k = 0; k < 8; k += 2)
+                        unpack2(fma2(pack2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), sk2,
+                                     pack2(nm[k], nm[k + 1])),
+                                x[8 * i + k], x[8 * i + k + 1]);
+                    if (masked) {
+                        const uint32_t w = rows_seeing(c);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            if (!((w >> k) & 1u)) x[8 * i + k] = -INFINITY;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) top = fmaxf(top, x[8 * i + k]);
+                }
+                if (named_or(wg_bar, 128, top > kGrow || fsv != 1.f)) {
+                    // move the maxima to the tile's, rescale the sums and O
+                    float keep = -INFINITY;             // lane 8 i + k: row k of chunk i
+#pragma unroll
+                    for (int i = 0; i < kChunks; ++i) {
+                        const int c = wg + 4 * i;
+                        if (c >= nch) break;
+                        uint32_t r[8];
+                        tc::tmem_ld8(t_lane + kColS + 128 * b + 8 * c, r);
+                        tc::tmem_wait_ld();
+                        const uint32_t w = masked ? rows_seeing(c) : 0xFFu;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float lg = ((w >> k) & 1u) ? __uint_as_float(r[k]) * skc : -INFINITY;
+                            x[8 * i + k] = lg;
+                            const float m = warp_redux_max(lg);
+                            if (lane == 8 * i + k) keep = m;
+                        }
+                    }
+                    const int row = 8 * (wg + 4 * (lane >> 3)) + (lane & 7);
+                    if (lane < 8 * kChunks) xch[128 * q4 + row] = keep;
+                    named_sync(wg_bar, 128);
+                    float cc = 1.f, nmx = 0.f;
+                    if (lane < 8 * kChunks) {
+                        const float old = -negm[row];
+                        nmx = fmaxf(fmaxf(fmaxf(xch[row], xch[128 + row]),
+                                          fmaxf(xch[256 + row], xch[384 + row])), old);
+                        cc = tc::ex2(old - nmx);
+                    }
+                    named_sync(wg_bar, 128);
+                    if (q4 == 0 && lane < 8 * kChunks) negm[row] = -nmx;
+                    if (j > 0) wait(pv_done((it - 1) & 1), ((it - 1) >> 1) & 1);
+                    tc::fence_after_sync();
+#pragma unroll
+                    for (int i = 0; i < kChunks; ++i) {
+                        const int c = wg + 4 * i;
+                        if (c >= nch) break;
+                        uint32_t o[8] = {};
+                        if (j > 0) {
+                            tc::tmem_ld8(t_lane + kColO + 8 * c, o);
+                            tc::tmem_wait_ld();
+                        }
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float f = __shfl_sync(kFull, cc, 8 * i + k);
+                            x[8 * i + k] -= __shfl_sync(kFull, nmx, 8 * i + k);
+                            lp[8 * i + k] *= f;
+                            o[k] = __float_as_uint(__uint_as_float(o[k]) * (f * fsv));
+                        }
+                        if (j > 0) tc::tmem_st8(t_lane + kColO + 8 * c, o);
+                    }
+                    tc::tmem_wait_st();
+                    named_sync(wg_bar, 128);            // the new maxima are in place
+                }
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(s_empty(b));
+                const uint32_t pt = sbase + kOffP + 32768 * b + t * 128;
+#pragma unroll
+                for (int i = 0; i < kChunks; ++i) {
+                    const int c = wg + 4 * i;
+                    if (c >= nch) break;
+                    float y[8];
+#pragma unroll
+                    for (int k = 0; k < 8; k += 2) {
+                        const uint64_t pr = pack2(tc::ex2(x[8 * i + k]), tc::ex2(x[8 * i + k + 1]));
+                        unpack2(add2(pack2(lp[8 * i + k], lp[8 * i + k + 1]), pr), lp[8 * i + k],
+                                lp[8 * i + k + 1]);
+                        unpack2(mul2(pr, sv2), y[k], y[k + 1]);
+                    }
+                    if (masked) {                       // a hidden block's scale may be anything
+                        const uint32_t w = rows_seeing(c);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            if (!((w >> k) & 1u)) y[k] = 0.f;
+                    }
+                    const uint32_t at = pt + (c >> 3) * 16384 + (((c & 7) ^ (t & 7)) << 4);
+                    uint32_t h[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) h[k] = half2_bits(y[2 * k], y[2 * k + 1]);
+                    dmq::sts128(at, h[0], h[1], h[2], h[3]);
+                    if constexpr (kTerms == 2) {
+                        uint32_t lo[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[k]));
+                            lo[k] = half2_bits(y[2 * k] - f.x, y[2 * k + 1] - f.y);
+                        }
+                        dmq::sts128(at + 16384, lo[0], lo[1], lo[2], lo[3]);
+                    }
+                }
+                fence_proxy_async();                    // read by the tensor core
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full(b));
+            }
+
+            // ---- the block's rows: thread = position of a dimension ----------
+            const int last = it - 1;
+            wait(pv_done(last & 1), (last >> 1) & 1);
+            tc::fence_after_sync();
+            const float ps = tps[2 * (last & 1) + 1];
+            // sum_t P'_t (2n - 15) 2^-11 -> sum_t p S_v (2n - 15) / 15
+            const float back = (ps > 0.f ? pow2_inv(ps) : 1.0f) * (2048.0f / 15.0f);
+            {
+                float v[32];
+#pragma unroll
+                for (int k = 0; k < 32; ++k) v[k] = k < 8 * kChunks ? lp[k < 8 * kChunks ? k : 0] : 0.f;
+                const float part = transpose_sum(v, lane);
+                const int row = 8 * (wg + 4 * (lane >> 3)) + (lane & 7);
+                if (lane < 8 * kChunks) xch[128 * q4 + row] = part;
+                named_sync(wg_bar, 128);
+                if (q4 == 0 && lane < 8 * kChunks && row < s.rows) {
+                    const float L = (xch[row] + xch[128 + row]) + (xch[256 + row] + xch[384 + row]);
+                    if (whole) {
+                        linv[row] = L == 0.f ? 0.f : 1.0f / L;
+                    } else {
+                        p.part_ml[(int64_t)part_slot(s, cta) * p.rows + row] = make_float2(-negm[row], L);
+                    }
+                }
+            }
+            const int d = dim_at(t);
+            float *stage = reinterpret_cast<float *>(smem + kOffV);      // [rows][128], V is done with
+            float *po = p.part_o + (int64_t)part_slot(s, cta) * p.rows * kD;
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) {
+                const int c = wg + 4 * i;
+                if (c >= nch) break;
+                uint32_t o[8];
+                tc::tmem_ld8(t_lane + kColO + 8 * c, o);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int row = 8 * c + k;
+                    if (row < s.rows) (whole ? stage : po)[row * kD + d] = __uint_as_float(o[k]) * back;
+                }
+            }
+            tc::fence_before_sync();
+            if (whole) {
+                named_sync(3, kSoftWarps * 32);
+                for (int r = ws; r < s.rows; r += kSoftWarps) {
+                    const float4 o = *reinterpret_cast<const float4 *>(stage + r * kD + 4 * lane);
+                    const float inv = linv[r];
+                    float v[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
+                    store_out(p, s.b, s.g, s.row0 + r, v, lane);
+                }
+            }
+            all_sync();
+        }
+    }
+}
+
+}  // namespace tree
+}  // namespace tbq4

@@ -12,7 +12,7 @@
 #include "decode_mq.cuh"
 #include "prefill_tc.cuh"
 #include "rope_append.cuh"
-#include "decode_tree.cuh"
+#include "decode_tree_tc.cuh"
 #include "tree_accept.cuh"
 #include "selftest.cuh"
 
@@ -754,8 +754,9 @@ tbq4_status rope_impl(const Rows &q, const Rows &k, const Rows &v, int dtype, in
     return launch_status();
 }
 
-// Rows per block of tree attention.
-int tree_rows(int) { return tree::kPlainRows; }
+// Rows per block of tree attention: fp16 outputs take two terms per operand
+// and half the rows (see tree_tc_kernel).
+int tree_rows(int out_dtype) { return out_dtype == TBQ4_F16 ? 64 : 128; }
 
 size_t tree_ws_bytes(int rows) {
     return align_up((size_t)2 * kNumSMs * rows * (kD * sizeof(float) + sizeof(float2)), kWsAlign);
@@ -821,12 +822,26 @@ tbq4_status tree_impl(const void *q, int q_dtype, const uint8_t *k, const uint8_
     p.out = out;
     p.out_type = out_dtype;
     p.out_elems = (int64_t)B * T * Hq * kD;
-    static bool attr_set[64] = {};
-    if (!ensure_smem_attr((const void *)tree::tree_plain_kernel, tree::kPlainSmem, attr_set))
-        return TBQ4_ERR_LAUNCH;
+    static bool attr1[64] = {}, attr2[64] = {};
+    const bool two = out_dtype == TBQ4_F16;
+    const void *fn = two ? (const void *)tree::tree_tc_kernel<2> : (const void *)tree::tree_tc_kernel<1>;
+    if (!ensure_smem_attr(fn, tree::kTcSmem, two ? attr2 : attr1)) return TBQ4_ERR_LAUNCH;
+    // the kernel moves registers between its warpgroups (setmaxnreg), which
+    // is safe only from the count it was written for
+    static int regs_ok[2] = {-1, -1};
+    if (regs_ok[two] < 0) {
+        cudaFuncAttributes fa;
+        regs_ok[two] = cudaFuncGetAttributes(&fa, fn) == cudaSuccess &&
+                       fa.numRegs >= tree::kLaunchRegs &&
+                       fa.numRegs * tree::kTcThreads <= 65536;
+    }
+    if (!regs_ok[two]) return TBQ4_ERR_LAUNCH;
     cudaStream_t st = (cudaStream_t)stream;
     if (g_ev_before) cudaEventRecord(g_ev_before, st);
-    tree::tree_plain_kernel<<<p.n_ctas, tree::kPlainWarps * 32, tree::kPlainSmem, st>>>(p);
+    if (two)
+        tree::tree_tc_kernel<2><<<p.n_ctas, tree::kTcThreads, tree::kTcSmem, st>>>(p);
+    else
+        tree::tree_tc_kernel<1><<<p.n_ctas, tree::kTcThreads, tree::kTcSmem, st>>>(p);
     // the join, a programmatic dependent launch: one CTA per start of a share
     // and group of rows
     cudaLaunchConfig_t cfg = {};

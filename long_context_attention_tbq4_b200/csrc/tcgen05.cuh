@@ -139,6 +139,21 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {
            ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
+// MN-major operand tile of 16-bit elements with 128-byte swizzle: rows of K,
+// each 128 bytes (64 elements along M or N) apart, in 8-row groups of 1024
+// bytes (stride byte offset); the next 64 elements along M or N start `lbo`
+// bytes further (leading byte offset).
+__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t lbo) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(lbo >> 4) << 16) |
+           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+// D f32, A and B fp16; bits 15 and 16: A, B MN-major.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool mn_major) {
+    return (1u << 4) | (mn_major ? (3u << 15) : 0u) | ((uint32_t)(N >> 3) << 17) |
+           ((uint32_t)(M >> 4) << 24);
+}
+
 // D f32, A and B bf16, both K-major.
 __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N) {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) |
