@@ -61,7 +61,7 @@ constexpr float kLowest = -1e30f;                       // running maximum befor
 // registers per thread by warpgroup: control, levels (2), softmax (4)
 // (setmaxnreg draws on what the block was launched with: the host refuses to
 // launch a build that compiled to fewer than kLaunchRegs)
-constexpr uint32_t kRegCtl = 24, kRegLev = 48, kRegSoft = 96;
+constexpr uint32_t kRegCtl = 56, kRegLev = 64, kRegSoft = 80;
 constexpr int kLaunchRegs = 72;
 static_assert(4 * kRegCtl + 8 * kRegLev + 16 * kRegSoft <= 28 * kLaunchRegs, "register split");
 
@@ -588,35 +588,39 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
                                      : node < s.n ? vis[4 * node + (c >> 2)] : 0u;
                     return w >> (8 * (c & 3));
                 };
-                float x[8 * kChunks];
-                float top = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < kChunks; ++i) {
-                    const int c = wg + 4 * i;
-                    if (c >= nch) break;
+                // log2 p of the 8 rows of chunk c: S skc - m, hidden ones -inf.  S is
+                // read twice, once for the vote and once for the weights: registers
+                // for 32 logits a thread do not fit beside the row sums
+                auto logits = [&](int c, float (&x)[8]) {
                     uint32_t r[8];
                     tc::tmem_ld8(t_lane + kColS + 128 * b + 8 * c, r);
                     const float4 n0 = *reinterpret_cast<const float4 *>(negm + 8 * c);
                     const float4 n1 = *reinterpret_cast<const float4 *>(negm + 8 * c + 4);
-                    tc::tmem_wait_ld();
                     const float nm[8] = {n0.x, n0.y, n0.z, n0.w, n1.x, n1.y, n1.z, n1.w};
+                    tc::tmem_wait_ld();
 #pragma unroll
                     for (int k = 0; k < 8; k += 2)
                         unpack2(fma2(pack2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), sk2,
-                                     pack2(nm[k], nm[k + 1])),
-                                x[8 * i + k], x[8 * i + k + 1]);
+                                     pack2(nm[k], nm[k + 1])), x[k], x[k + 1]);
                     if (masked) {
                         const uint32_t w = rows_seeing(c);
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
-                            if (!((w >> k) & 1u)) x[8 * i + k] = -INFINITY;
+                            if (!((w >> k) & 1u)) x[k] = -INFINITY;
                     }
+                };
+                float top = -INFINITY;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) top = fmaxf(top, x[8 * i + k]);
+                for (int i = 0; i < kChunks; ++i) {
+                    if (wg + 4 * i >= nch) break;
+                    float x[8];
+                    logits(wg + 4 * i, x);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) top = fmaxf(top, x[k]);
                 }
                 if (named_or(wg_bar, 128, top > kGrow || fsv != 1.f)) {
                     // move the maxima to the tile's, rescale the sums and O
-                    float keep = -INFINITY;             // lane 8 i + k: row k of chunk i
+                    float keep = kLowest;               // lane 8 i + k: row k of chunk i
 #pragma unroll
                     for (int i = 0; i < kChunks; ++i) {
                         const int c = wg + 4 * i;
@@ -627,9 +631,8 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
                         const uint32_t w = masked ? rows_seeing(c) : 0xFFu;
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
-                            const float lg = ((w >> k) & 1u) ? __uint_as_float(r[k]) * skc : -INFINITY;
-                            x[8 * i + k] = lg;
-                            const float m = warp_redux_max(lg);
+                            const float m = warp_redux_max(((w >> k) & 1u) ? __uint_as_float(r[k]) * skc
+                                                                           : -INFINITY);
                             if (lane == 8 * i + k) keep = m;
                         }
                     }
@@ -659,7 +662,6 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
                             const float f = __shfl_sync(kFull, cc, 8 * i + k);
-                            x[8 * i + k] -= __shfl_sync(kFull, nmx, 8 * i + k);
                             lp[8 * i + k] *= f;
                             o[k] = __float_as_uint(__uint_as_float(o[k]) * (f * fsv));
                         }
@@ -668,18 +670,16 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
                     tc::tmem_wait_st();
                     named_sync(wg_bar, 128);            // the new maxima are in place
                 }
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(s_empty(b));
                 const uint32_t pt = sbase + kOffP + 32768 * b + t * 128;
 #pragma unroll
                 for (int i = 0; i < kChunks; ++i) {
                     const int c = wg + 4 * i;
                     if (c >= nch) break;
                     float y[8];
+                    logits(c, y);
 #pragma unroll
                     for (int k = 0; k < 8; k += 2) {
-                        const uint64_t pr = pack2(tc::ex2(x[8 * i + k]), tc::ex2(x[8 * i + k + 1]));
+                        const uint64_t pr = pack2(tc::ex2(y[k]), tc::ex2(y[k + 1]));
                         unpack2(add2(pack2(lp[8 * i + k], lp[8 * i + k + 1]), pr), lp[8 * i + k],
                                 lp[8 * i + k + 1]);
                         unpack2(mul2(pr, sv2), y[k], y[k + 1]);
@@ -708,7 +708,10 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
                 fence_proxy_async();                    // read by the tensor core
                 tc::fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(p_full(b));
+                if (lane == 0) {
+                    mbar_arrive(s_empty(b));
+                    mbar_arrive(p_full(b));
+                }
             }
 
             // ---- the block's rows: thread = position of a dimension ----------
