@@ -31,15 +31,18 @@
 //
 // Softmax.  thread = token, so its S_k and S_v are scalars and a row's
 // running maximum is one number for all threads (shared memory).  The
-// maximum moves only when a logit exceeds it by 2^3 in log2 units: one
-// barrier-with-vote per tile decides that, and the rare path takes the tile's
-// maxima and rescales O.  Sums stay in registers until the end.  Tiles that
-// hold drafted nodes or the end of the sequence apply masks by select, to
-// logits and to weights (a hidden block may hold anything).
+// maximum moves only when a logit exceeds it by 8 in log2 units: one
+// barrier-with-vote per 32 rows of a warpgroup decides that, and the rare path
+// takes the tile's maxima and rescales O.  Sums stay in registers until the
+// end.  Tiles that hold drafted nodes or the end of the sequence apply masks
+// by select, to logits and to weights (a hidden block may hold anything).
 //
-// Warps (28): 0 producer (cp.async.bulk, 32-token pieces), 1 tensor-memory
-// allocation and every tcgen05.mma, 4-7 K levels, 8-11 V levels, 12-27
-// softmax (four warpgroups; 8-row chunk c belongs to warpgroup c % 4).
+// Warps (20): 0 producer (cp.async.bulk, 32-token pieces), 1 tensor-memory
+// allocation and every tcgen05.mma, 4-7 K levels and both scales, 8-11 V
+// levels, 12-19 softmax (two warpgroups; 8-row chunk c belongs to warpgroup
+// c % 2).  The softmax waits for one barrier per tile: the commit behind
+// S(j) covers PV(j - 2), which read the P' buffer it will write, and the
+// scales come with the K levels.
 // Hand-offs are mbarriers with bounded waits; a warp whose wait runs out
 // records the error and goes on without waiting, so the named barriers of
 // its warpgroup and of the CTA always fill.
@@ -50,20 +53,20 @@
 namespace tbq4 {
 namespace tree {
 
-constexpr int kTcThreads = 896;
-constexpr int kSoftWarp0 = 12, kSoftWarps = 16;
+constexpr int kTcThreads = 640;
+constexpr int kSoftWarp0 = 12, kSoftWarps = 8;
 constexpr int kRaw = 3;                                 // raw tiles in flight, K and V each
 constexpr int kRawTile = kTileT * kBlockBytes;          // 8448
 constexpr int kRawStride = kRawTile + 16;
 constexpr uint32_t kSpinTree = 1u << 22;
 constexpr float kGrow = 8.0f;                           // log2 units
 constexpr float kLowest = -1e30f;                       // running maximum before any token
-// registers per thread by warpgroup: control, levels (2), softmax (4)
+// registers per thread by warpgroup: control, levels (2), softmax (2)
 // (setmaxnreg draws on what the block was launched with: the host refuses to
 // launch a build that compiled to fewer than kLaunchRegs)
-constexpr uint32_t kRegCtl = 56, kRegLev = 64, kRegSoft = 80;
-constexpr int kLaunchRegs = 72;
-static_assert(4 * kRegCtl + 8 * kRegLev + 16 * kRegSoft <= 28 * kLaunchRegs, "register split");
+constexpr uint32_t kRegCtl = 56, kRegLev = 56, kRegSoft = 152;
+constexpr int kLaunchRegs = 96;
+static_assert(4 * kRegCtl + 8 * kRegLev + 8 * kRegSoft <= 20 * kLaunchRegs, "register split");
 
 constexpr int kOffQ = 0;                                // 32 KB: kTerms x rows x 256 B
 constexpr int kOffP = 32768;                            // 2 x 32 KB: kTerms x rows/64 x 16 KB
@@ -152,6 +155,12 @@ __device__ __forceinline__ int dim_at(int pos) {
     return (pos & ~7) | ((pos & 1) << 2) | ((pos & 7) >> 1);
 }
 
+// Width of the products for a block of `rows` rows: each warpgroup takes
+// whole chunks of 8, in the counts that soft_segment is compiled for.
+__device__ __forceinline__ int tile_rows(int rows) {
+    return rows <= 64 ? (rows + 15) & ~15 : (rows + 31) & ~31;
+}
+
 // Sum over the warp of 32 values per lane: lane l gets the sum of v[l].
 __device__ __forceinline__ float transpose_sum(float (&v)[32], int lane) {
 #pragma unroll
@@ -166,11 +175,225 @@ __device__ __forceinline__ float transpose_sum(float (&v)[32], int lane) {
     return v[0];
 }
 
+__device__ __forceinline__ float4 lds128f(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ float ldsf(uint32_t a) { return __uint_as_float(dmq::lds32(a)); }
+__device__ __forceinline__ void stsf(uint32_t a, float x) {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(x) : "memory");
+}
+
+// Bounded wait of one warp: false once one has run out, and from then on at
+// once (the error is recorded the first time).
+__device__ __forceinline__ void wait_or_fail(bool &ok, uint32_t bar, uint32_t parity) {
+    if (ok && !mbar_wait_bounded(bar, parity, kSpinTree)) {
+        ok = false;
+        record_status(7u /* TBQ4_ERR_DEVICE_TIMEOUT */);
+    }
+}
+
+// What a softmax thread keeps across the tiles of a segment.
+struct Soft {
+    uint32_t sbase, tmem, bx;               // shared memory, tensor memory, first hand-off barrier
+    int t, lane, wg;                        // token of the tile, lane, warpgroup
+    float c2;                               // log2 logit = S S_k c2
+};
+
+// One tile for kN chunks of 8 rows (chunks wg, wg + 2, ..).  The rows go in
+// groups of up to four chunks, whose 32 logits stay in registers between the
+// vote and the weights.  kMasked: the tile holds drafted nodes or ends the
+// sequence; `node` is then this token's node (below 0: context).
+template <int kTerms, int kN, bool kMasked>
+__device__ __forceinline__ void soft_tile(const Soft &c, int it, bool first, int node, int n_nodes,
+                                          float (&lp)[8 * kN], bool &ok) {
+    const int b = it & 1;
+    wait_or_fail(ok, c.bx + 8 * (2 + b), (it >> 1) & 1);           // S, and the scales with it
+    tc::fence_after_sync();
+    const uint32_t q_lane = (uint32_t)(c.t & ~31) << 16;
+    const uint32_t s_col = c.tmem + q_lane + kColS + 128 * b, o_col = c.tmem + q_lane + kColO;
+    const float skc = ldsf(c.sbase + kOffSig + (kTileT * b + c.t) * 4) * c.c2;
+    const float svp = ldsf(c.sbase + kOffSig + (kTileT * (2 + b) + c.t) * 4);
+    const float fsv = ldsf(c.sbase + kOffPs + 8 * b);
+    const uint64_t sk2 = pack2(skc, skc), sv2 = pack2(svp, svp);
+    uint32_t see[4];                                               // rows that see this token
+    if constexpr (kMasked) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+            see[w] = node < 0 ? 0xFFFFFFFFu
+                   : node < n_nodes ? dmq::lds32(c.sbase + kOffVis + 16 * node + 4 * w) : 0u;
+    }
+    auto sees = [&](int i, int k) -> bool {                        // row k of chunk wg + 2 i
+        if constexpr (!kMasked) return true;
+        return (see[i >> 1] >> (8 * ((c.wg + 2 * i) & 3) + k)) & 1u;
+    };
+    const uint32_t pt = c.sbase + kOffP + 32768 * b + c.t * 128;
+#pragma unroll
+    for (int i0 = 0; i0 < kN; i0 += 4) {
+        constexpr int kG = kN < 4 ? kN : 4;
+        const int n = kN - i0 < kG ? kN - i0 : kG;                 // constant once unrolled
+        uint32_t r[kG][8];
+        auto load = [&]() {
+#pragma unroll
+            for (int i = 0; i < kG; ++i)
+                if (i < n) tc::tmem_ld8(s_col + 8 * (c.wg + 2 * (i0 + i)), r[i]);
+            tc::tmem_wait_ld();
+        };
+        // log2 p: S skc - m, hidden ones -inf
+        auto logits = [&]() {
+#pragma unroll
+            for (int i = 0; i < kG; ++i) {
+                if (i >= n) continue;
+                const uint32_t at = c.sbase + kOffNegM + 32 * (c.wg + 2 * (i0 + i));
+                const float4 n0 = lds128f(at), n1 = lds128f(at + 16);
+                const float nm[8] = {n0.x, n0.y, n0.z, n0.w, n1.x, n1.y, n1.z, n1.w};
+#pragma unroll
+                for (int k = 0; k < 8; k += 2) {
+                    float x0, x1;
+                    unpack2(fma2(pack2(__uint_as_float(r[i][k]), __uint_as_float(r[i][k + 1])), sk2,
+                                 pack2(nm[k], nm[k + 1])), x0, x1);
+                    r[i][k] = sees(i0 + i, k) ? __float_as_uint(x0) : 0xFF800000u;
+                    r[i][k + 1] = sees(i0 + i, k + 1) ? __float_as_uint(x1) : 0xFF800000u;
+                }
+            }
+        };
+        load();
+        logits();
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kG; ++i)
+            if (i < n) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) top = fmaxf(top, __uint_as_float(r[i][k]));
+            }
+        if (__builtin_expect(named_or(4 + c.wg, 128, top > kGrow || fsv != 1.f), 0)) {
+            // move the maxima to the tile's, rescale the sums and O
+            load();
+            float keep = kLowest;                                  // lane 8 i + k: row k of chunk i
+#pragma unroll
+            for (int i = 0; i < kG; ++i) {
+                if (i >= n) continue;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float m = warp_redux_max(
+                        sees(i0 + i, k) ? __uint_as_float(r[i][k]) * skc : -INFINITY);
+                    if (c.lane == 8 * i + k) keep = m;
+                }
+            }
+            const uint32_t row = 8 * (c.wg + 2 * (i0 + (c.lane >> 3))) + (c.lane & 7);
+            const bool mine = (c.lane >> 3) < n;
+            const uint32_t xch = c.sbase + kOffXch + 4 * row, nega = c.sbase + kOffNegM + 4 * row;
+            if (mine) stsf(xch + 512 * (c.t >> 5), keep);
+            named_sync(4 + c.wg, 128);
+            float cc = 1.f, nmx = 0.f;
+            if (mine) {
+                const float old = -ldsf(nega);
+                nmx = fmaxf(fmaxf(fmaxf(ldsf(xch), ldsf(xch + 512)), fmaxf(ldsf(xch + 1024), ldsf(xch + 1536))),
+                            old);
+                cc = tc::ex2(old - nmx);
+            }
+            named_sync(4 + c.wg, 128);
+            if (mine && c.t < 32) stsf(nega, -nmx);
+            if (!first) wait_or_fail(ok, c.bx + 8 * (10 + ((it - 1) & 1)), ((it - 1) >> 1) & 1);
+            tc::fence_after_sync();
+#pragma unroll
+            for (int i = 0; i < kG; ++i) {
+                if (i >= n) continue;
+                uint32_t o[8] = {};
+                const uint32_t col = o_col + 8 * (c.wg + 2 * (i0 + i));
+                if (!first) {
+                    tc::tmem_ld8(col, o);
+                    tc::tmem_wait_ld();
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float f = __shfl_sync(kFull, cc, 8 * i + k);
+                    lp[8 * (i0 + i) + k] *= f;
+                    o[k] = __float_as_uint(__uint_as_float(o[k]) * (f * fsv));
+                }
+                if (!first) tc::tmem_st8(col, o);
+            }
+            tc::tmem_wait_st();
+            named_sync(4 + c.wg, 128);                             // the new maxima are in place
+            load();
+            logits();
+        }
+#pragma unroll
+        for (int i = 0; i < kG; ++i) {
+            if (i >= n) continue;
+            const int ch = c.wg + 2 * (i0 + i);
+            float y[8];
+#pragma unroll
+            for (int k = 0; k < 8; k += 2) {
+                float &l0 = lp[8 * (i0 + i) + k], &l1 = lp[8 * (i0 + i) + k + 1];
+                const uint64_t pr = pack2(tc::ex2(__uint_as_float(r[i][k])),
+                                          tc::ex2(__uint_as_float(r[i][k + 1])));
+                unpack2(add2(pack2(l0, l1), pr), l0, l1);
+                unpack2(mul2(pr, sv2), y[k], y[k + 1]);
+                if constexpr (kMasked) {                           // a hidden block may hold anything
+                    if (!sees(i0 + i, k)) y[k] = 0.f;
+                    if (!sees(i0 + i, k + 1)) y[k + 1] = 0.f;
+                }
+            }
+            const uint32_t at = pt + (ch >> 3) * 16384 + (((ch & 7) ^ (c.t & 7)) << 4);
+            uint32_t h[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) h[k] = half2_bits(y[2 * k], y[2 * k + 1]);
+            dmq::sts128(at, h[0], h[1], h[2], h[3]);
+            if constexpr (kTerms == 2) {
+                uint32_t lo[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[k]));
+                    lo[k] = half2_bits(y[2 * k] - f.x, y[2 * k + 1] - f.y);
+                }
+                dmq::sts128(at + 16384, lo[0], lo[1], lo[2], lo[3]);
+            }
+        }
+    }
+    fence_proxy_async();                                           // read by the tensor core
+    tc::fence_before_sync();
+    __syncwarp();
+    if (c.lane == 0) {
+        mbar_arrive(c.bx + 8 * (4 + b));                           // S and the scales are read
+        mbar_arrive(c.bx + 8 * (8 + b));                           // P' is written
+    }
+}
+
+// The tiles of a segment, and each row's sum into xch[quarter][row].  A
+// loop for the tiles that every row sees in full and one for the last one or
+// two, so that the frequent one is short straight code.
+template <int kTerms, int kN>
+__device__ __forceinline__ void soft_segment(const Soft &c, int it, int tiles, int t0, int ctx,
+                                             int n_nodes, bool &ok) {
+    float lp[8 * kN];
+#pragma unroll
+    for (int k = 0; k < 8 * kN; ++k) lp[k] = 0.f;
+    const int full = min(tiles, max(0, (ctx - t0) / kTileT));
+    int j = 0;
+#pragma unroll 1
+    for (; j < full; ++j) soft_tile<kTerms, kN, false>(c, it + j, j == 0, 0, 0, lp, ok);
+#pragma unroll 1
+    for (; j < tiles; ++j)
+        soft_tile<kTerms, kN, true>(c, it + j, j == 0, t0 + j * kTileT + c.t - ctx, n_nodes, lp, ok);
+#pragma unroll
+    for (int i0 = 0; i0 < kN; i0 += 4) {
+        float v[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) v[k] = 8 * i0 + k < 8 * kN ? lp[8 * i0 + k < 8 * kN ? 8 * i0 + k : 0] : 0.f;
+        const float sum = transpose_sum(v, c.lane);
+        if (i0 + (c.lane >> 3) < kN)
+            stsf(c.sbase + kOffXch + 512 * (c.t >> 5) +
+                     4 * (8 * (c.wg + 2 * (i0 + (c.lane >> 3))) + (c.lane & 7)), sum);
+    }
+}
+
 template <int kTerms>
 __global__ void __launch_bounds__(kTcThreads, 1)
 tree_tc_kernel(const __grid_constant__ TreeParams p) {
     constexpr int kRows = 128 / kTerms;                 // rows per block, at most
-    constexpr int kChunks = kRows / 32;                 // 8-row chunks per warpgroup, at most
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -213,7 +436,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
             mbar_init(kraw_full(s), 1);
             mbar_init(kraw_empty(s), 4);
             mbar_init(vraw_full(s), 1);
-            mbar_init(vraw_empty(s), 4);
+            mbar_init(vraw_empty(s), 8);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(k_full(b), 4);
@@ -237,15 +460,10 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
     const uint32_t tmem = *tmem_ptr;
 
     bool ok = true;                                     // this warp's waits have all come through
-    auto wait = [&](uint32_t bar, uint32_t parity) {
-        if (ok && !mbar_wait_bounded(bar, parity, kSpinTree)) {
-            ok = false;
-            record_status(7u /* TBQ4_ERR_DEVICE_TIMEOUT */);
-        }
-    };
+    auto wait = [&](uint32_t bar, uint32_t parity) { wait_or_fail(ok, bar, parity); };
     // everyone but the producer and the two idle warps, at the start of a
     // segment (twice) and at its end
-    auto all_sync = [&]() { named_sync(1, 25 * 32); };
+    auto all_sync = [&]() { named_sync(1, 17 * 32); };
 
     if (warp < 4) {
         tc::regs_dec<kRegCtl>();
@@ -297,7 +515,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
             for (int u = u0; u < u1;) {
                 const Segment s = segment_at(p, prefix, u, u1);
                 u += s.tiles;
-                const int N = (s.rows + 15) & ~15;
+                const int N = tile_rows(s.rows);
                 const uint32_t idesc_qk = tc::idesc_f16(128, N, false);
                 const uint32_t idesc_pv = tc::idesc_f16(128, N, true);
                 all_sync();
@@ -390,20 +608,43 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
                 }
                 vis[e] = bits;
             }
+            const int stop = s.ctx + s.n;
+            float ps = 0.f;                             // 0 until a nonzero V scale arrives
             all_sync();
             all_sync();
             for (int j = 0; j < s.tiles; ++j, ++it) {
                 const int st = it % kRaw, b = it & 1;
                 wait(kraw_full(st), (it / kRaw) & 1);
-                // the softmax has read S and S_k of tile it - 2, so its product
-                // is done with this K buffer
-                if (it >= 2) wait(s_empty(b), ((it >> 1) - 1) & 1);
-                tc::fence_after_sync();
+                wait(vraw_full(st), (it / kRaw) & 1);
                 const uint32_t row = sbase + kOffRawK + st * kRawStride + t * kBlockBytes;
-                sig_k[kTileT * b + t] = half_bits_to_float((uint16_t)dmq::lds16(row));
+                const float sk = half_bits_to_float((uint16_t)dmq::lds16(row));
+                const float sv = (s.tile0 + j) * kTileT + t < stop
+                    ? half_bits_to_float((uint16_t)dmq::lds16(row + kOffRawV - kOffRawK)) : 0.f;
+                // the tile's largest finite V scale
+                const float mine = warp_redux_max(isfinite(sv) ? sv : 0.f);
+                if (lane == 0) vmax[4 * b + (warp & 3)] = mine;
+                // the softmax has read S and the scales of tile it - 2, so its
+                // product is done with this K buffer
+                if (it >= 2) wait(s_empty(b), ((it >> 1) - 1) & 1);
+                named_sync(2, 128);
+                tc::fence_after_sync();
+                const float4 m4 = *reinterpret_cast<const float4 *>(vmax + 4 * b);
+                const float top = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
+                float f = 1.f;
+                if (ps == 0.f ? top > 0.f : top * ps > 128.0f) {
+                    const float nps = pow2_floor(__fdividef(128.0f, top));
+                    f = ps == 0.f ? 1.f : pow2_ratio(nps, ps);
+                    ps = nps;
+                }
+                sig_k[kTileT * b + t] = sk;
+                sig_v[kTileT * b + t] = sv * ps;
+                if (t == 0) {
+                    tps[2 * b] = f;
+                    tps[2 * b + 1] = ps;
+                }
                 const uint32_t a0 = (row + 2) & ~3u, sh = ((row + 2) & 3u) * 8u;
                 uint32_t w = dmq::lds32(a0);
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < 4; ++c) {           // four words: 32 levels, 16 columns
                     uint32_t o[16];
 #pragma unroll
@@ -423,6 +664,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
                 if (lane == 0) {
                     mbar_arrive(k_full(b));
                     mbar_arrive(kraw_empty(st));
+                    mbar_arrive(vraw_empty(st));
                 }
             }
             all_sync();
@@ -435,8 +677,6 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
         for (int u = u0; u < u1;) {
             const Segment s = segment_at(p, prefix, u, u1);
             u += s.tiles;
-            const int stop = s.ctx + s.n;
-            float ps = 0.f;                             // 0 until a nonzero scale arrives
             all_sync();
             all_sync();
             for (int j = 0; j < s.tiles; ++j, ++it) {
@@ -444,29 +684,10 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
                 wait(vraw_full(st), (it / kRaw) & 1);
                 if (it >= 2) wait(pv_done(b), ((it >> 1) - 1) & 1);
                 const uint32_t row = sbase + kOffRawV + st * kRawStride + t * kBlockBytes;
-                const float sv = (s.tile0 + j) * kTileT + t < stop
-                    ? half_bits_to_float((uint16_t)dmq::lds16(row)) : 0.f;
-                // the tile's largest finite scale
-                const float mine = warp_redux_max(isfinite(sv) ? sv : 0.f);
-                if (lane == 0) vmax[4 * b + (warp & 3)] = mine;
-                named_sync(2, 128);
-                const float4 m4 = *reinterpret_cast<const float4 *>(vmax + 4 * b);
-                const float top = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
-                float f = 1.f;
-                if (ps == 0.f ? top > 0.f : top * ps > 128.0f) {
-                    const float nps = pow2_floor(__fdividef(128.0f, top));
-                    f = ps == 0.f ? 1.f : pow2_ratio(nps, ps);
-                    ps = nps;
-                }
-                sig_v[kTileT * b + t] = sv * ps;
-                if (t == 0) {
-                    tps[2 * b] = f;
-                    tps[2 * b + 1] = ps;
-                }
                 const uint32_t a0 = (row + 2) & ~3u, sh = ((row + 2) & 3u) * 8u;
                 const uint32_t to = sbase + kOffV + 32768 * b + t * 128;
                 uint32_t w = dmq::lds32(a0);
-#pragma unroll
+#pragma unroll 4
                 for (int c = 0; c < 16; ++c) {          // a word: eight levels, 16 bytes
                     const uint32_t nx = dmq::lds32(a0 + 4 * (c + 1));
                     uint32_t l[4];
@@ -496,7 +717,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
             const Segment s = segment_at(p, prefix, u, u1);
             const bool whole = s.tiles == s.work_tiles;
             u += s.tiles;
-            const int N = (s.rows + 15) & ~15, nch = N >> 3;
+            const int N = tile_rows(s.rows), nch = N >> 3;
             // ---- queries: rotate, agree on the power of two, store -----------
             float ql[kRows / kSoftWarps][4];
             float mx = 0.f;
@@ -518,7 +739,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
             }
             mx = warp_max(mx);
             if (lane == 0 && mx > 0.f) atomicMax(qmax, __float_as_uint(mx));
-            if (ws * 8 < kRows && lane < 8) negm[ws * 8 + lane] = -kLowest;
+            for (int r = ws * 32 + lane; r < kRows; r += 32 * kSoftWarps) negm[r] = -kLowest;
             all_sync();
             const float big = __uint_as_float(*qmax);
             int e2 = 0;
@@ -558,161 +779,22 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
             all_sync();
             if (ws == 0 && lane == 0) *qmax = 0u;       // for the next segment (read before the barrier)
 
-            float lp[8 * kChunks];
-#pragma unroll
-            for (int k = 0; k < 8 * kChunks; ++k) lp[k] = 0.f;
-            for (int j = 0; j < s.tiles; ++j, ++it) {
-                const int b = it & 1;
-                const uint32_t par = (it >> 1) & 1;
-                const int ta = (s.tile0 + j) * kTileT;
-                const bool masked = ta + kTileT > s.ctx;
-                wait(s_full(b), par);
-                wait(k_full(b), par);
-                wait(v_full(b), par);
-                tc::fence_after_sync();
-                if (wg >= nch) {                        // no rows for this warpgroup
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(s_empty(b));
-                        mbar_arrive(p_full(b));
+            const Soft sc = {sbase, tmem, bx, t, lane, wg, c2};
+            const int t0 = s.tile0 * kTileT;
+            switch (N >> 4) {                           // chunks of this warpgroup
+                case 1: soft_segment<kTerms, 1>(sc, it, s.tiles, t0, s.ctx, s.n, ok); break;
+                case 2: soft_segment<kTerms, 2>(sc, it, s.tiles, t0, s.ctx, s.n, ok); break;
+                case 3: soft_segment<kTerms, 3>(sc, it, s.tiles, t0, s.ctx, s.n, ok); break;
+                case 4: soft_segment<kTerms, 4>(sc, it, s.tiles, t0, s.ctx, s.n, ok); break;
+                default:
+                    if constexpr (kTerms == 1) {
+                        if (N <= 96)
+                            soft_segment<kTerms, 6>(sc, it, s.tiles, t0, s.ctx, s.n, ok);
+                        else
+                            soft_segment<kTerms, 8>(sc, it, s.tiles, t0, s.ctx, s.n, ok);
                     }
-                    continue;
-                }
-                const float skc = sig_k[kTileT * b + t] * c2, svp = sig_v[kTileT * b + t];
-                const float fsv = tps[2 * b];
-                const uint64_t sk2 = pack2(skc, skc), sv2 = pack2(svp, svp);
-                // the word of rows that see this token, for chunk c
-                auto rows_seeing = [&](int c) -> uint32_t {
-                    const int node = ta + t - s.ctx;
-                    const uint32_t w = node < 0 ? 0xFFFFFFFFu
-                                     : node < s.n ? vis[4 * node + (c >> 2)] : 0u;
-                    return w >> (8 * (c & 3));
-                };
-                // log2 p of the 8 rows of chunk c: S skc - m, hidden ones -inf.  S is
-                // read twice, once for the vote and once for the weights: registers
-                // for 32 logits a thread do not fit beside the row sums
-                auto logits = [&](int c, float (&x)[8]) {
-                    uint32_t r[8];
-                    tc::tmem_ld8(t_lane + kColS + 128 * b + 8 * c, r);
-                    const float4 n0 = *reinterpret_cast<const float4 *>(negm + 8 * c);
-                    const float4 n1 = *reinterpret_cast<const float4 *>(negm + 8 * c + 4);
-                    const float nm[8] = {n0.x, n0.y, n0.z, n0.w, n1.x, n1.y, n1.z, n1.w};
-                    tc::tmem_wait_ld();
-#pragma unroll
-                    for (int k = 0; k < 8; k += 2)
-                        unpack2(fma2(pack2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), sk2,
-                                     pack2(nm[k], nm[k + 1])), x[k], x[k + 1]);
-                    if (masked) {
-                        const uint32_t w = rows_seeing(c);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            if (!((w >> k) & 1u)) x[k] = -INFINITY;
-                    }
-                };
-                float top = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < kChunks; ++i) {
-                    if (wg + 4 * i >= nch) break;
-                    float x[8];
-                    logits(wg + 4 * i, x);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) top = fmaxf(top, x[k]);
-                }
-                if (named_or(wg_bar, 128, top > kGrow || fsv != 1.f)) {
-                    // move the maxima to the tile's, rescale the sums and O
-                    float keep = kLowest;               // lane 8 i + k: row k of chunk i
-#pragma unroll
-                    for (int i = 0; i < kChunks; ++i) {
-                        const int c = wg + 4 * i;
-                        if (c >= nch) break;
-                        uint32_t r[8];
-                        tc::tmem_ld8(t_lane + kColS + 128 * b + 8 * c, r);
-                        tc::tmem_wait_ld();
-                        const uint32_t w = masked ? rows_seeing(c) : 0xFFu;
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const float m = warp_redux_max(((w >> k) & 1u) ? __uint_as_float(r[k]) * skc
-                                                                           : -INFINITY);
-                            if (lane == 8 * i + k) keep = m;
-                        }
-                    }
-                    const int row = 8 * (wg + 4 * (lane >> 3)) + (lane & 7);
-                    if (lane < 8 * kChunks) xch[128 * q4 + row] = keep;
-                    named_sync(wg_bar, 128);
-                    float cc = 1.f, nmx = 0.f;
-                    if (lane < 8 * kChunks) {
-                        const float old = -negm[row];
-                        nmx = fmaxf(fmaxf(fmaxf(xch[row], xch[128 + row]),
-                                          fmaxf(xch[256 + row], xch[384 + row])), old);
-                        cc = tc::ex2(old - nmx);
-                    }
-                    named_sync(wg_bar, 128);
-                    if (q4 == 0 && lane < 8 * kChunks) negm[row] = -nmx;
-                    if (j > 0) wait(pv_done((it - 1) & 1), ((it - 1) >> 1) & 1);
-                    tc::fence_after_sync();
-#pragma unroll
-                    for (int i = 0; i < kChunks; ++i) {
-                        const int c = wg + 4 * i;
-                        if (c >= nch) break;
-                        uint32_t o[8] = {};
-                        if (j > 0) {
-                            tc::tmem_ld8(t_lane + kColO + 8 * c, o);
-                            tc::tmem_wait_ld();
-                        }
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const float f = __shfl_sync(kFull, cc, 8 * i + k);
-                            lp[8 * i + k] *= f;
-                            o[k] = __float_as_uint(__uint_as_float(o[k]) * (f * fsv));
-                        }
-                        if (j > 0) tc::tmem_st8(t_lane + kColO + 8 * c, o);
-                    }
-                    tc::tmem_wait_st();
-                    named_sync(wg_bar, 128);            // the new maxima are in place
-                }
-                const uint32_t pt = sbase + kOffP + 32768 * b + t * 128;
-#pragma unroll
-                for (int i = 0; i < kChunks; ++i) {
-                    const int c = wg + 4 * i;
-                    if (c >= nch) break;
-                    float y[8];
-                    logits(c, y);
-#pragma unroll
-                    for (int k = 0; k < 8; k += 2) {
-                        const uint64_t pr = pack2(tc::ex2(y[k]), tc::ex2(y[k + 1]));
-                        unpack2(add2(pack2(lp[8 * i + k], lp[8 * i + k + 1]), pr), lp[8 * i + k],
-                                lp[8 * i + k + 1]);
-                        unpack2(mul2(pr, sv2), y[k], y[k + 1]);
-                    }
-                    if (masked) {                       // a hidden block's scale may be anything
-                        const uint32_t w = rows_seeing(c);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            if (!((w >> k) & 1u)) y[k] = 0.f;
-                    }
-                    const uint32_t at = pt + (c >> 3) * 16384 + (((c & 7) ^ (t & 7)) << 4);
-                    uint32_t h[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) h[k] = half2_bits(y[2 * k], y[2 * k + 1]);
-                    dmq::sts128(at, h[0], h[1], h[2], h[3]);
-                    if constexpr (kTerms == 2) {
-                        uint32_t lo[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[k]));
-                            lo[k] = half2_bits(y[2 * k] - f.x, y[2 * k + 1] - f.y);
-                        }
-                        dmq::sts128(at + 16384, lo[0], lo[1], lo[2], lo[3]);
-                    }
-                }
-                fence_proxy_async();                    // read by the tensor core
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(s_empty(b));
-                    mbar_arrive(p_full(b));
-                }
             }
+            it += s.tiles;
 
             // ---- the block's rows: thread = position of a dimension ----------
             const int last = it - 1;
@@ -721,29 +803,22 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
             const float ps = tps[2 * (last & 1) + 1];
             // sum_t P'_t (2n - 15) 2^-11 -> sum_t p S_v (2n - 15) / 15
             const float back = (ps > 0.f ? pow2_inv(ps) : 1.0f) * (2048.0f / 15.0f);
-            {
-                float v[32];
-#pragma unroll
-                for (int k = 0; k < 32; ++k) v[k] = k < 8 * kChunks ? lp[k < 8 * kChunks ? k : 0] : 0.f;
-                const float part = transpose_sum(v, lane);
-                const int row = 8 * (wg + 4 * (lane >> 3)) + (lane & 7);
-                if (lane < 8 * kChunks) xch[128 * q4 + row] = part;
-                named_sync(wg_bar, 128);
-                if (q4 == 0 && lane < 8 * kChunks && row < s.rows) {
-                    const float L = (xch[row] + xch[128 + row]) + (xch[256 + row] + xch[384 + row]);
-                    if (whole) {
-                        linv[row] = L == 0.f ? 0.f : 1.0f / L;
-                    } else {
-                        p.part_ml[(int64_t)part_slot(s, cta) * p.rows + row] = make_float2(-negm[row], L);
-                    }
-                }
+            named_sync(wg_bar, 128);
+            for (int r = t; r < 64; r += 128) {
+                const int row = 8 * (wg + 2 * (r >> 3)) + (r & 7);
+                if (row >= s.rows) break;
+                const float L = (xch[row] + xch[128 + row]) + (xch[256 + row] + xch[384 + row]);
+                if (whole)
+                    linv[row] = L == 0.f ? 0.f : 1.0f / L;
+                else
+                    p.part_ml[(int64_t)part_slot(s, cta) * p.rows + row] = make_float2(-negm[row], L);
             }
             const int d = dim_at(t);
             float *stage = reinterpret_cast<float *>(smem + kOffV);      // [rows][128], V is done with
             float *po = p.part_o + (int64_t)part_slot(s, cta) * p.rows * kD;
 #pragma unroll
-            for (int i = 0; i < kChunks; ++i) {
-                const int c = wg + 4 * i;
+            for (int i = 0; i < kRows / 16; ++i) {
+                const int c = wg + 2 * i;
                 if (c >= nch) break;
                 uint32_t o[8];
                 tc::tmem_ld8(t_lane + kColO + 8 * c, o);
