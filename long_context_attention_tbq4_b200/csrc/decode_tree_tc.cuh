@@ -58,6 +58,7 @@ constexpr int kSoftWarp0 = 12, kSoftWarps = 8;
 constexpr int kRaw = 3;                                 // raw tiles in flight, K and V each
 constexpr int kRawTile = kTileT * kBlockBytes;          // 8448
 constexpr int kRawStride = kRawTile + 16;
+constexpr int kSig = 4;                                 // tiles whose scales are kept
 constexpr uint32_t kSpinTree = 1u << 22;
 constexpr float kGrow = 8.0f;                           // log2 units
 constexpr float kLowest = -1e30f;                       // running maximum before any token
@@ -73,13 +74,13 @@ constexpr int kOffP = 32768;                            // 2 x 32 KB: kTerms x r
 constexpr int kOffV = kOffP + 2 * 32768;                // 2 x 32 KB
 constexpr int kOffRawK = kOffV + 2 * 32768;
 constexpr int kOffRawV = kOffRawK + kRaw * kRawStride;
-constexpr int kOffSig = kOffRawV + kRaw * kRawStride;   // S_k, S_v ps: [2][2][128] floats
-constexpr int kOffNegM = kOffSig + 2 * 2 * kTileT * 4;  // minus the running maxima [128]
+constexpr int kOffSig = kOffRawV + kRaw * kRawStride;   // S_k, S_v ps: [2][4][128] floats
+constexpr int kOffNegM = kOffSig + 2 * kSig * kTileT * 4;  // minus the running maxima [128]
 constexpr int kOffXch = kOffNegM + 128 * 4;             // [4][128] floats
 constexpr int kOffLinv = kOffXch + 4 * 128 * 4;         // [128] floats
 constexpr int kOffVis = kOffLinv + 128 * 4;             // [64 nodes][4] words: rows that see it
-constexpr int kOffPs = kOffVis + kMaxNodes * 16;        // [2] x (factor, ps)
-constexpr int kOffMax = kOffPs + 16;                    // [2][4] floats: V scales
+constexpr int kOffPs = kOffVis + kMaxNodes * 16;        // [4] x (factor, ps)
+constexpr int kOffMax = kOffPs + 8 * kSig;                    // [2][4] floats: V scales
 constexpr int kOffQMax = kOffMax + 32;                  // bits of the largest |q_rot|
 constexpr int kOffTmem = kOffQMax + 8;
 constexpr int kOffBars = kOffTmem + 8;
@@ -195,6 +196,17 @@ __device__ __forceinline__ void wait_or_fail(bool &ok, uint32_t bar, uint32_t pa
     }
 }
 
+// The same for the warps that run ahead of the softmax: they sleep between
+// polls, which leaves the schedulers to it (tight polling by the level and
+// copy warps was a quarter of all instructions).
+constexpr uint32_t kLazyTree = 64;                      // nanoseconds
+__device__ __forceinline__ void lazy_or_fail(bool &ok, uint32_t bar, uint32_t parity) {
+    if (ok && !mbar_wait_lazy_warp(bar, parity, kSpinTree, kLazyTree)) {
+        ok = false;
+        record_status(7u /* TBQ4_ERR_DEVICE_TIMEOUT */);
+    }
+}
+
 // What a softmax thread keeps across the tiles of a segment.
 struct Soft {
     uint32_t sbase, tmem, bx;               // shared memory, tensor memory, first hand-off barrier
@@ -202,8 +214,8 @@ struct Soft {
     float c2;                               // log2 logit = S S_k c2
 };
 
-// One tile for kN chunks of 8 rows (chunks wg, wg + 2, ..).  The rows go in
-// groups of up to four chunks, whose 32 logits stay in registers between the
+// One tile for kN chunks of 8 rows (chunks wg, wg + 2, ..), in one group or,
+// at eight, in two of four: a group's logits stay in registers between the
 // vote and the weights.  kMasked: the tile holds drafted nodes or ends the
 // sequence; `node` is then this token's node (below 0: context).
 template <int kTerms, int kN, bool kMasked>
@@ -214,11 +226,12 @@ __device__ __forceinline__ void soft_tile(const Soft &c, int it, bool first, int
     tc::fence_after_sync();
     const uint32_t q_lane = (uint32_t)(c.t & ~31) << 16;
     const uint32_t s_col = c.tmem + q_lane + kColS + 128 * b, o_col = c.tmem + q_lane + kColO;
-    const float skc = ldsf(c.sbase + kOffSig + (kTileT * b + c.t) * 4) * c.c2;
-    const float svp = ldsf(c.sbase + kOffSig + (kTileT * (2 + b) + c.t) * 4);
-    const float fsv = ldsf(c.sbase + kOffPs + 8 * b);
+    const int sg = it & (kSig - 1);
+    const float skc = ldsf(c.sbase + kOffSig + (kTileT * sg + c.t) * 4) * c.c2;
+    const float svp = ldsf(c.sbase + kOffSig + (kTileT * (kSig + sg) + c.t) * 4);
+    const float fsv = ldsf(c.sbase + kOffPs + 8 * sg);
     const uint64_t sk2 = pack2(skc, skc), sv2 = pack2(svp, svp);
-    uint32_t see[4];                                               // rows that see this token
+    uint32_t see[4] = {};                                          // rows that see this token
     if constexpr (kMasked) {
 #pragma unroll
         for (int w = 0; w < 4; ++w)
@@ -226,13 +239,15 @@ __device__ __forceinline__ void soft_tile(const Soft &c, int it, bool first, int
                    : node < n_nodes ? dmq::lds32(c.sbase + kOffVis + 16 * node + 4 * w) : 0u;
     }
     auto sees = [&](int i, int k) -> bool {                        // row k of chunk wg + 2 i
-        if constexpr (!kMasked) return true;
-        return (see[i >> 1] >> (8 * ((c.wg + 2 * i) & 3) + k)) & 1u;
+        if constexpr (kMasked)
+            return (see[i >> 1] >> (8 * ((c.wg + 2 * i) & 3) + k)) & 1u;
+        else
+            return true;
     };
     const uint32_t pt = c.sbase + kOffP + 32768 * b + c.t * 128;
 #pragma unroll
-    for (int i0 = 0; i0 < kN; i0 += 4) {
-        constexpr int kG = kN < 4 ? kN : 4;
+    for (int i0 = 0; i0 < kN; i0 += kN <= 6 ? kN : 4) {
+        constexpr int kG = kN <= 6 ? kN : 4;
         const int n = kN - i0 < kG ? kN - i0 : kG;                 // constant once unrolled
         uint32_t r[kG][8];
         auto load = [&]() {
@@ -269,33 +284,46 @@ __device__ __forceinline__ void soft_tile(const Soft &c, int it, bool first, int
                 for (int k = 0; k < 8; ++k) top = fmaxf(top, __uint_as_float(r[i][k]));
             }
         if (__builtin_expect(named_or(4 + c.wg, 128, top > kGrow || fsv != 1.f), 0)) {
-            // move the maxima to the tile's, rescale the sums and O
+            // move the maxima to the tile's, rescale the sums and O: rounds of
+            // four chunks, lane 8 i + k for row k of the round's chunk i
+            constexpr int kRounds = (kG + 3) / 4;
             load();
-            float keep = kLowest;                                  // lane 8 i + k: row k of chunk i
+            float keep[kRounds], cc[kRounds], nmx[kRounds];
 #pragma unroll
             for (int i = 0; i < kG; ++i) {
+                if (i % 4 == 0) keep[i / 4] = kLowest;
                 if (i >= n) continue;
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     const float m = warp_redux_max(
                         sees(i0 + i, k) ? __uint_as_float(r[i][k]) * skc : -INFINITY);
-                    if (c.lane == 8 * i + k) keep = m;
+                    if (c.lane == 8 * (i % 4) + k) keep[i / 4] = m;
                 }
             }
-            const uint32_t row = 8 * (c.wg + 2 * (i0 + (c.lane >> 3))) + (c.lane & 7);
-            const bool mine = (c.lane >> 3) < n;
-            const uint32_t xch = c.sbase + kOffXch + 4 * row, nega = c.sbase + kOffNegM + 4 * row;
-            if (mine) stsf(xch + 512 * (c.t >> 5), keep);
+            auto row_of = [&](int round) -> uint32_t {
+                return 8 * (c.wg + 2 * (i0 + 4 * round + (c.lane >> 3))) + (c.lane & 7);
+            };
+            auto in = [&](int round) -> bool { return 4 * round + (c.lane >> 3) < n; };
+            const uint32_t xch = c.sbase + kOffXch, nega = c.sbase + kOffNegM;
+#pragma unroll
+            for (int g = 0; g < kRounds; ++g)
+                if (in(g)) stsf(xch + 512 * (c.t >> 5) + 4 * row_of(g), keep[g]);
             named_sync(4 + c.wg, 128);
-            float cc = 1.f, nmx = 0.f;
-            if (mine) {
-                const float old = -ldsf(nega);
-                nmx = fmaxf(fmaxf(fmaxf(ldsf(xch), ldsf(xch + 512)), fmaxf(ldsf(xch + 1024), ldsf(xch + 1536))),
-                            old);
-                cc = tc::ex2(old - nmx);
+#pragma unroll
+            for (int g = 0; g < kRounds; ++g) {
+                cc[g] = 1.f;
+                nmx[g] = 0.f;
+                if (!in(g)) continue;
+                const uint32_t at = xch + 4 * row_of(g);
+                const float old = -ldsf(nega + 4 * row_of(g));
+                nmx[g] = fmaxf(fmaxf(fmaxf(ldsf(at), ldsf(at + 512)), fmaxf(ldsf(at + 1024), ldsf(at + 1536))),
+                               old);
+                cc[g] = tc::ex2(old - nmx[g]);
             }
             named_sync(4 + c.wg, 128);
-            if (mine && c.t < 32) stsf(nega, -nmx);
+#pragma unroll
+            for (int g = 0; g < kRounds; ++g)
+                if (in(g) && c.t < 32) stsf(nega + 4 * row_of(g), -nmx[g]);
             if (!first) wait_or_fail(ok, c.bx + 8 * (10 + ((it - 1) & 1)), ((it - 1) >> 1) & 1);
             tc::fence_after_sync();
 #pragma unroll
@@ -309,7 +337,7 @@ __device__ __forceinline__ void soft_tile(const Soft &c, int it, bool first, int
                 }
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    const float f = __shfl_sync(kFull, cc, 8 * i + k);
+                    const float f = __shfl_sync(kFull, cc[i / 4], 8 * (i % 4) + k);
                     lp[8 * (i0 + i) + k] *= f;
                     o[k] = __float_as_uint(__uint_as_float(o[k]) * (f * fsv));
                 }
@@ -421,8 +449,8 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
     auto pv_done = [&](int b) { return bx + 8 * (10 + b); };    // V levels and P' read
     const uint32_t drained = bx + 8 * 12;
     uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(smem + kOffTmem);
-    float *sig_k = reinterpret_cast<float *>(smem + kOffSig);       // [2][128]
-    float *sig_v = sig_k + 2 * kTileT;                              // [2][128]
+    float *sig_k = reinterpret_cast<float *>(smem + kOffSig);       // [4][128]
+    float *sig_v = sig_k + kSig * kTileT;                           // [4][128]
     float *negm = reinterpret_cast<float *>(smem + kOffNegM);
     float *xch = reinterpret_cast<float *>(smem + kOffXch);
     float *linv = reinterpret_cast<float *>(smem + kOffLinv);
@@ -461,6 +489,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
 
     bool ok = true;                                     // this warp's waits have all come through
     auto wait = [&](uint32_t bar, uint32_t parity) { wait_or_fail(ok, bar, parity); };
+    auto lazy = [&](uint32_t bar, uint32_t parity) { lazy_or_fail(ok, bar, parity); };
     // everyone but the producer and the two idle warps, at the start of a
     // segment (twice) and at its end
     auto all_sync = [&]() { named_sync(1, 17 * 32); };
@@ -477,8 +506,8 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
                 for (int j = 0; j < s.tiles; ++j, ++it) {
                     const int st = it % kRaw;
                     if (it >= kRaw) {
-                        wait(kraw_empty(st), ((it / kRaw) - 1) & 1);
-                        wait(vraw_empty(st), ((it / kRaw) - 1) & 1);
+                        lazy(kraw_empty(st), ((it / kRaw) - 1) & 1);
+                        lazy(vraw_empty(st), ((it / kRaw) - 1) & 1);
                         if (!ok) break;
                     }
                     const int t = (s.tile0 + j) * kTileT;
@@ -521,68 +550,74 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
                 all_sync();
                 all_sync();
                 tc::fence_after_sync();
-                if (lane == 0) {
-                    int jq = 0, jp = 0;                 // next QK and PV of this segment
-                    uint32_t idle = 0;
-                    while (ok && jp < s.tiles) {
-                        bool moved = false;
-                        if (jq < s.tiles && jq <= jp + 1) {
-                            const int it = it0 + jq, b = it & 1;
-                            if (mbar_test(k_full(b), (it >> 1) & 1) &&
-                                (it < 2 || mbar_test(s_empty(b), ((it >> 1) - 1) & 1))) {
-                                tc::fence_after_sync();
+                // the whole warp runs the loop, one elected lane issues
+                const bool leader = tc::elect_one();
+                const uint64_t q_desc = tc::desc_sw128(sbase + kOffQ);
+                const uint64_t v_desc = tc::desc_mn_sw128(sbase + kOffV, 16384);
+                const uint64_t p_desc = tc::desc_mn_sw128(sbase + kOffP, 16384);
+                int jq = 0, jp = 0;                     // next QK and PV of this segment
+                uint32_t idle = 0;
+                while (ok && jp < s.tiles) {
+                    bool moved = false;
+                    if (jq < s.tiles && jq <= jp + 1) {
+                        const int it = it0 + jq, b = it & 1;
+                        if (__all_sync(kFull, mbar_test(k_full(b), (it >> 1) & 1) &&
+                                       (it < 2 || mbar_test(s_empty(b), ((it >> 1) - 1) & 1)))) {
+                            tc::fence_after_sync();
+                            if (leader) {
+                                const uint32_t d = tmem + kColS + 128 * b, ka = tmem + kColK + 64 * b;
+                                tc::mma_ts_c<false>(d, ka, q_desc, idesc_qk);
 #pragma unroll
-                                for (int i = 0; i < 8 * kTerms; ++i) {
-                                    const int ki = i & 7;
-                                    tc::mma_ts(tmem + kColS + 128 * b, tmem + kColK + 64 * b + 8 * ki,
-                                               tc::desc_sw128(sbase + kOffQ + (i >> 3) * (kRows * 256) +
-                                                              (ki >> 2) * (kRows * 128) + (ki & 3) * 32),
-                                               idesc_qk, i > 0);
-                                }
+                                for (int i = 1; i < 8 * kTerms; ++i)     // descriptors count 16 bytes
+                                    tc::mma_ts_c<true>(d, ka + 8 * (i & 7),
+                                                       q_desc + (i >> 3) * (kRows * 16) +
+                                                           ((i & 7) >> 2) * (kRows * 8) + (i & 3) * 2,
+                                                       idesc_qk);
                                 tc::mma_commit(s_full(b));
-                                ++jq;
-                                moved = true;
                             }
+                            __syncwarp();
+                            ++jq;
+                            moved = true;
                         }
-                        if (jp < jq) {
-                            const int it = it0 + jp, b = it & 1;
-                            if (mbar_test(p_full(b), (it >> 1) & 1) &&
-                                mbar_test(v_full(b), (it >> 1) & 1)) {
-                                tc::fence_after_sync();
-                                const uint32_t vt = sbase + kOffV + 32768 * b;
-                                const uint32_t pt = sbase + kOffP + 32768 * b;
+                    }
+                    if (jp < jq) {
+                        const int it = it0 + jp, b = it & 1;
+                        if (__all_sync(kFull, mbar_test(p_full(b), (it >> 1) & 1) &&
+                                       mbar_test(v_full(b), (it >> 1) & 1))) {
+                            tc::fence_after_sync();
+                            if (leader) {
+                                const uint64_t va = v_desc + 2048 * b, pb = p_desc + 2048 * b;
+                                if (jp > 0)
+                                    tc::mma_ss_c<true>(tmem + kColO, va, pb, idesc_pv);
+                                else
+                                    tc::mma_ss_c<false>(tmem + kColO, va, pb, idesc_pv);
 #pragma unroll
-                                for (int i = 0; i < 8 * kTerms; ++i)
-                                    tc::mma_ss(tmem + kColO,
-                                               tc::desc_mn_sw128(vt + 2048 * (i & 7), 16384),
-                                               tc::desc_mn_sw128(pt + (i >> 3) * 16384 + 2048 * (i & 7),
-                                                                 16384),
-                                               idesc_pv, (jp > 0 || i > 0) ? 1u : 0u);
+                                for (int i = 1; i < 8 * kTerms; ++i)
+                                    tc::mma_ss_c<true>(tmem + kColO, va + 128 * (i & 7),
+                                                       pb + (i >> 3) * 1024 + 128 * (i & 7), idesc_pv);
                                 tc::mma_commit(pv_done(b));
-                                ++jp;
-                                moved = true;
                             }
+                            __syncwarp();
+                            ++jp;
+                            moved = true;
                         }
-                        if (moved) {
-                            idle = 0;
-                        } else {
-                            __nanosleep(20);
-                            if (++idle > kSpinTree) {
-                                ok = false;
-                                record_status(7u);
-                            }
+                    }
+                    if (moved) {
+                        idle = 0;
+                    } else {
+                        __nanosleep(20);
+                        if (++idle > kSpinTree) {
+                            ok = false;
+                            if (lane == 0) record_status(7u);
                         }
                     }
                 }
-                __syncwarp();
                 it0 += s.tiles;
                 all_sync();
             }
-            if (lane == 0) {                            // every product issued has ended
-                tc::mma_commit(drained);
-                mbar_wait_thread(drained, 0, kSpinTree);
-            }
+            if (tc::elect_one()) tc::mma_commit(drained);    // every product issued has ended
             __syncwarp();
+            mbar_wait_bounded(drained, 0, kSpinTree);
             tc::fence_after_sync();
             tc::tmem_dealloc(tmem, 512);
         }
@@ -623,11 +658,12 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
                 // the tile's largest finite V scale
                 const float mine = warp_redux_max(isfinite(sv) ? sv : 0.f);
                 if (lane == 0) vmax[4 * b + (warp & 3)] = mine;
-                // the softmax has read S and the scales of tile it - 2, so its
-                // product is done with this K buffer
-                if (it >= 2) wait(s_empty(b), ((it >> 1) - 1) & 1);
+                // the row's words, all in flight at once
+                const uint32_t a0 = (row + 2) & ~3u, sh = ((row + 2) & 3u) * 8u;
+                uint32_t w[17];
+#pragma unroll
+                for (int i = 0; i < 17; ++i) w[i] = dmq::lds32(a0 + 4 * i);
                 named_sync(2, 128);
-                tc::fence_after_sync();
                 const float4 m4 = *reinterpret_cast<const float4 *>(vmax + 4 * b);
                 const float top = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
                 float f = 1.f;
@@ -636,23 +672,24 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
                     f = ps == 0.f ? 1.f : pow2_ratio(nps, ps);
                     ps = nps;
                 }
-                sig_k[kTileT * b + t] = sk;
-                sig_v[kTileT * b + t] = sv * ps;
+                // QK(it - 2) has read this K buffer, and was issued after the
+                // softmax had read tile it - 4's scales
+                if (it >= 2) wait(s_full(b), ((it >> 1) - 1) & 1);
+                tc::fence_after_sync();
+                const int sg = it & (kSig - 1);
+                sig_k[kTileT * sg + t] = sk;
+                sig_v[kTileT * sg + t] = sv * ps;
                 if (t == 0) {
-                    tps[2 * b] = f;
-                    tps[2 * b + 1] = ps;
+                    tps[2 * sg] = f;
+                    tps[2 * sg + 1] = ps;
                 }
-                const uint32_t a0 = (row + 2) & ~3u, sh = ((row + 2) & 3u) * 8u;
-                uint32_t w = dmq::lds32(a0);
-#pragma unroll 1
+#pragma unroll
                 for (int c = 0; c < 4; ++c) {           // four words: 32 levels, 16 columns
                     uint32_t o[16];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const uint32_t nx = dmq::lds32(a0 + 4 * (4 * c + i + 1));
                         uint32_t l[4];
-                        word_levels(__funnelshift_r(w, nx, sh), l);
-                        w = nx;
+                        word_levels(__funnelshift_r(w[4 * c + i], w[4 * c + i + 1], sh), l);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) o[4 * i + e] = l[e];
                     }
@@ -682,18 +719,19 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
             for (int j = 0; j < s.tiles; ++j, ++it) {
                 const int st = it % kRaw, b = it & 1;
                 wait(vraw_full(st), (it / kRaw) & 1);
-                if (it >= 2) wait(pv_done(b), ((it >> 1) - 1) & 1);
                 const uint32_t row = sbase + kOffRawV + st * kRawStride + t * kBlockBytes;
                 const uint32_t a0 = (row + 2) & ~3u, sh = ((row + 2) & 3u) * 8u;
-                const uint32_t to = sbase + kOffV + 32768 * b + t * 128;
-                uint32_t w = dmq::lds32(a0);
-#pragma unroll 4
+                uint32_t w[17];
+#pragma unroll
+                for (int i = 0; i < 17; ++i) w[i] = dmq::lds32(a0 + 4 * i);
+                if (it >= 2) wait(pv_done(b), ((it >> 1) - 1) & 1);
+                // 16-byte chunk c of row t lies at c ^ (t % 8)
+                const uint32_t to = sbase + kOffV + 32768 * b + t * 128 + ((t & 7) << 4);
+#pragma unroll
                 for (int c = 0; c < 16; ++c) {          // a word: eight levels, 16 bytes
-                    const uint32_t nx = dmq::lds32(a0 + 4 * (c + 1));
                     uint32_t l[4];
-                    word_levels(__funnelshift_r(w, nx, sh), l);
-                    w = nx;
-                    dmq::sts128(to + (c >> 3) * 16384 + (((c & 7) ^ (t & 7)) << 4), l[0], l[1], l[2], l[3]);
+                    word_levels(__funnelshift_r(w[c], w[c + 1], sh), l);
+                    dmq::sts128((to ^ ((c & 7) << 4)) + (c >> 3) * 16384, l[0], l[1], l[2], l[3]);
                 }
                 fence_proxy_async();                    // read by the tensor core
                 __syncwarp();
@@ -800,7 +838,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
             const int last = it - 1;
             wait(pv_done(last & 1), (last >> 1) & 1);
             tc::fence_after_sync();
-            const float ps = tps[2 * (last & 1) + 1];
+            const float ps = tps[2 * (last & (kSig - 1)) + 1];
             // sum_t P'_t (2n - 15) 2^-11 -> sum_t p S_v (2n - 15) / 15
             const float back = (ps > 0.f ? pow2_inv(ps) : 1.0f) * (2048.0f / 15.0f);
             named_sync(wg_bar, 128);
