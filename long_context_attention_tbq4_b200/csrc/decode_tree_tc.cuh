@@ -630,18 +630,23 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
         for (int u = u0; u < u1;) {
             const Segment s = segment_at(p, prefix, u, u1);
             u += s.tiles;
-            // rows of the block that see node j, one bit each (word w: rows 32 w ..)
-            for (int e = t; e < kMaxNodes * 4; e += 128) {
-                const int j = e >> 2, c0 = s.row0 + 32 * (e & 3);
-                uint32_t bits = 0;
-                if (j < s.n) {
-                    int i = c0 / p.G, h = c0 - i * p.G;
-                    for (int k = 0; k < 32 && i < s.n; ++k) {
-                        bits |= (uint32_t)((__ldg(p.mask + s.b * p.mask_stride + i) >> j) & 1ull) << k;
-                        if (++h == p.G) { h = 0; ++i; }
+            // rows of the block that see node j, one bit each: lane = row 32 w +
+            // lane with its node's mask, a vote per node
+            {
+                const int w = warp & 3, c = 32 * w + lane;
+                unsigned long long m = 0ull;
+                if (c < s.rows) m = __ldg(p.mask + s.b * p.mask_stride + (s.row0 + c) / p.G);
+#pragma unroll 1
+                for (int jh = 0; jh < 2; ++jh) {
+                    const uint32_t half = (uint32_t)(m >> (32 * jh));
+                    uint32_t mine = 0;
+#pragma unroll 8
+                    for (int k = 0; k < 32; ++k) {
+                        const uint32_t v = __ballot_sync(kFull, (half >> k) & 1u);
+                        if (lane == k) mine = v;
                     }
+                    vis[4 * (32 * jh + lane) + w] = mine;
                 }
-                vis[e] = bits;
             }
             const int stop = s.ctx + s.n;
             float ps = 0.f;                             // 0 until a nonzero V scale arrives
@@ -658,11 +663,11 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
                 // the tile's largest finite V scale
                 const float mine = warp_redux_max(isfinite(sv) ? sv : 0.f);
                 if (lane == 0) vmax[4 * b + (warp & 3)] = mine;
-                // the row's words, all in flight at once
+                // the row's words, four ahead of their use
                 const uint32_t a0 = (row + 2) & ~3u, sh = ((row + 2) & 3u) * 8u;
-                uint32_t w[17];
+                uint32_t w[5];
 #pragma unroll
-                for (int i = 0; i < 17; ++i) w[i] = dmq::lds32(a0 + 4 * i);
+                for (int i = 0; i < 5; ++i) w[i] = dmq::lds32(a0 + 4 * i);
                 named_sync(2, 128);
                 const float4 m4 = *reinterpret_cast<const float4 *>(vmax + 4 * b);
                 const float top = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
@@ -683,17 +688,22 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
                     tps[2 * sg] = f;
                     tps[2 * sg + 1] = ps;
                 }
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < 4; ++c) {           // four words: 32 levels, 16 columns
-                    uint32_t o[16];
+                    uint32_t o[16], nx[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) nx[i] = dmq::lds32(a0 + 4 * min(4 * c + 5 + i, 16));
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         uint32_t l[4];
-                        word_levels(__funnelshift_r(w[4 * c + i], w[4 * c + i + 1], sh), l);
+                        word_levels(__funnelshift_r(w[i], w[i + 1], sh), l);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) o[4 * i + e] = l[e];
                     }
                     tc::tmem_st16(t_lane + kColK + 64 * b + 16 * c, o);
+                    w[0] = w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) w[i + 1] = nx[i];
                 }
                 tc::tmem_wait_st();
                 tc::fence_before_sync();
@@ -721,17 +731,27 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
                 wait(vraw_full(st), (it / kRaw) & 1);
                 const uint32_t row = sbase + kOffRawV + st * kRawStride + t * kBlockBytes;
                 const uint32_t a0 = (row + 2) & ~3u, sh = ((row + 2) & 3u) * 8u;
-                uint32_t w[17];
+                uint32_t w[5];
 #pragma unroll
-                for (int i = 0; i < 17; ++i) w[i] = dmq::lds32(a0 + 4 * i);
+                for (int i = 0; i < 5; ++i) w[i] = dmq::lds32(a0 + 4 * i);
                 if (it >= 2) wait(pv_done(b), ((it >> 1) - 1) & 1);
                 // 16-byte chunk c of row t lies at c ^ (t % 8)
                 const uint32_t to = sbase + kOffV + 32768 * b + t * 128 + ((t & 7) << 4);
+#pragma unroll 1
+                for (int c = 0; c < 16; c += 4) {       // a word: eight levels, 16 bytes
+                    uint32_t nx[4];
 #pragma unroll
-                for (int c = 0; c < 16; ++c) {          // a word: eight levels, 16 bytes
-                    uint32_t l[4];
-                    word_levels(__funnelshift_r(w[c], w[c + 1], sh), l);
-                    dmq::sts128((to ^ ((c & 7) << 4)) + (c >> 3) * 16384, l[0], l[1], l[2], l[3]);
+                    for (int i = 0; i < 4; ++i) nx[i] = dmq::lds32(a0 + 4 * min(c + 5 + i, 16));
+                    const uint32_t tc4 = (to ^ ((c & 4) << 4)) + (c >> 3) * 16384;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t l[4];
+                        word_levels(__funnelshift_r(w[i], w[i + 1], sh), l);
+                        dmq::sts128(tc4 ^ (i << 4), l[0], l[1], l[2], l[3]);
+                    }
+                    w[0] = w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) w[i + 1] = nx[i];
                 }
                 fence_proxy_async();                    // read by the tensor core
                 __syncwarp();
@@ -757,22 +777,34 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
             u += s.tiles;
             const int N = tile_rows(s.rows), nch = N >> 3;
             // ---- queries: rotate, agree on the power of two, store -----------
-            float ql[kRows / kSoftWarps][4];
+            // (rolled loops through shared memory: straight-line code that runs
+            // once per segment costs its instruction fetches, some 25 us at 16
+            // rows per warp)
+            float *stage = reinterpret_cast<float *>(smem + kOffV);   // [rows][128], no V in it yet
             float mx = 0.f;
+#pragma unroll 1
+            for (int r0 = ws; r0 < s.rows; r0 += 4 * kSoftWarps) {
+                float x[4][4];
 #pragma unroll
-            for (int k = 0; k < kRows / kSoftWarps; ++k) {
-                const int r = ws + kSoftWarps * k;
+                for (int k = 0; k < 4; ++k) {
+                    const int c = s.row0 + min(r0 + kSoftWarps * k, s.rows - 1);
+                    const int i = c / p.G, h = s.g * p.G + (c - i * p.G);
+                    load4(p.q, p.q_type, (((int64_t)s.b * p.T + i) * p.Hq + h) * kD + 4 * lane, x[k]);
+                }
+#pragma unroll 1
+                for (int k = 0; k < 4; ++k) {
+                    float y[4] = {x[0][0], x[0][1], x[0][2], x[0][3]};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) ql[k][e] = 0.f;
-                if (r < s.rows) {
-                    const int c = s.row0 + r, i = c / p.G, h = s.g * p.G + (c - i * p.G);
-                    load4(p.q, p.q_type, (((int64_t)s.b * p.T + i) * p.Hq + h) * kD + 4 * lane, ql[k]);
-                    warp_rotate128(ql[k], sbits, lane);
+                    for (int e = 0; e < 4; ++e) { x[0][e] = x[1][e]; x[1][e] = x[2][e]; x[2][e] = x[3][e]; }
+                    const int r = r0 + kSoftWarps * k;
+                    if (r >= s.rows) break;
+                    warp_rotate128(y, sbits, lane);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float a = fabsf(ql[k][e]);
+                        const float a = fabsf(y[e]);
                         if (isfinite(a)) mx = fmaxf(mx, a);
                     }
+                    *reinterpret_cast<float4 *>(stage + r * kD + 4 * lane) = make_float4(y[0], y[1], y[2], y[3]);
                 }
             }
             mx = warp_max(mx);
@@ -786,15 +818,18 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
             const float up = ldexpf(1.0f, 15 - e2);
             // log2 logit = S skc with skc = S_k c (levels are (2n - 15) 2^-11)
             const float c2 = p.scale * (1.4426950408889634f * 2048.0f / 15.0f) * ldexpf(1.0f, e2 - 15);
-#pragma unroll
-            for (int k = 0; k < kRows / kSoftWarps; ++k) {
-                const int r = ws + kSoftWarps * k;
-                if (r >= N) continue;
+#pragma unroll 1
+            for (int r = ws; r < N; r += kSoftWarps) {
                 // the operands' order of dimensions: pairs (d, d + 4) of each eight
                 const bool odd = lane & 1;
-                float x[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[e] = ql[k][e] * up;
+                float x[4] = {0.f, 0.f, 0.f, 0.f};
+                if (r < s.rows) {
+                    const float4 y = *reinterpret_cast<const float4 *>(stage + r * kD + 4 * lane);
+                    x[0] = y.x * up;
+                    x[1] = y.y * up;
+                    x[2] = y.z * up;
+                    x[3] = y.w * up;
+                }
                 const float g0 = __shfl_xor_sync(kFull, odd ? x[0] : x[2], 1);
                 const float g1 = __shfl_xor_sync(kFull, odd ? x[1] : x[3], 1);
                 const float a0 = odd ? g0 : x[0], b0 = odd ? x[2] : g0;
@@ -852,12 +887,9 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
                     p.part_ml[(int64_t)part_slot(s, cta) * p.rows + row] = make_float2(-negm[row], L);
             }
             const int d = dim_at(t);
-            float *stage = reinterpret_cast<float *>(smem + kOffV);      // [rows][128], V is done with
             float *po = p.part_o + (int64_t)part_slot(s, cta) * p.rows * kD;
-#pragma unroll
-            for (int i = 0; i < kRows / 16; ++i) {
-                const int c = wg + 2 * i;
-                if (c >= nch) break;
+#pragma unroll 1
+            for (int c = wg; c < nch; c += 2) {          // (V is done with its buffers)
                 uint32_t o[8];
                 tc::tmem_ld8(t_lane + kColO + 8 * c, o);
                 tc::tmem_wait_ld();
