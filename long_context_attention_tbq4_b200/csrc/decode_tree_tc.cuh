@@ -32,17 +32,19 @@
 // Softmax.  thread = token, so its S_k and S_v are scalars and a row's
 // running maximum is one number for all threads (shared memory).  The
 // maximum moves only when a logit exceeds it by 8 in log2 units: one
-// barrier-with-vote per 32 rows of a warpgroup decides that, and the rare path
+// barrier-with-vote per warpgroup and tile decides that, and the rare path
 // takes the tile's maxima and rescales O.  Sums stay in registers until the
 // end.  Tiles that hold drafted nodes or the end of the sequence apply masks
 // by select, to logits and to weights (a hidden block may hold anything).
 //
-// Warps (20): 0 producer (cp.async.bulk, 32-token pieces), 1 tensor-memory
-// allocation and every tcgen05.mma, 4-7 K levels and both scales, 8-11 V
-// levels, 12-19 softmax (two warpgroups; 8-row chunk c belongs to warpgroup
-// c % 2).  The softmax waits for one barrier per tile: the commit behind
-// S(j) covers PV(j - 2), which read the P' buffer it will write, and the
-// scales come with the K levels.
+// Warps (28): 0 producer (cp.async.bulk, 32-token pieces), 1 tensor-memory
+// allocation and every tcgen05.mma, 2 block scales, 4-7 and 8-11 levels (K
+// and V of the even and of the odd tiles), 12-27 softmax (four warpgroups;
+// 8-row chunk c belongs to warpgroup c % 4).  Every role is bound by latency
+// rather than by a unit, hence that many warps and the two level groups.
+// The softmax waits for one barrier per tile: QK(j) is issued once levels and
+// scales of tile j are there, and its commit covers PV(j - 2), which read the
+// P' buffer that the softmax will write.
 // Hand-offs are mbarriers with bounded waits; a warp whose wait runs out
 // records the error and goes on without waiting, so the named barriers of
 // its warpgroup and of the CTA always fill.
@@ -53,8 +55,8 @@
 namespace tbq4 {
 namespace tree {
 
-constexpr int kTcThreads = 640;
-constexpr int kSoftWarp0 = 12, kSoftWarps = 8;
+constexpr int kTcThreads = 896;
+constexpr int kSoftWarp0 = 12, kSoftWarps = 16;
 constexpr int kRaw = 3;                                 // raw tiles in flight, K and V each
 constexpr int kRawTile = kTileT * kBlockBytes;          // 8448
 constexpr int kRawStride = kRawTile + 16;
@@ -62,12 +64,12 @@ constexpr int kSig = 4;                                 // tiles whose scales ar
 constexpr uint32_t kSpinTree = 1u << 22;
 constexpr float kGrow = 8.0f;                           // log2 units
 constexpr float kLowest = -1e30f;                       // running maximum before any token
-// registers per thread by warpgroup: control, levels (2), softmax (2)
+// registers per thread by warpgroup: control, levels (2), softmax (4)
 // (setmaxnreg draws on what the block was launched with: the host refuses to
 // launch a build that compiled to fewer than kLaunchRegs)
-constexpr uint32_t kRegCtl = 56, kRegLev = 56, kRegSoft = 152;
-constexpr int kLaunchRegs = 96;
-static_assert(4 * kRegCtl + 8 * kRegLev + 8 * kRegSoft <= 20 * kLaunchRegs, "register split");
+constexpr uint32_t kRegCtl = 40, kRegLev = 40, kRegSoft = 96;
+constexpr int kLaunchRegs = 72;
+static_assert(4 * kRegCtl + 8 * kRegLev + 16 * kRegSoft <= 28 * kLaunchRegs, "register split");
 
 constexpr int kOffQ = 0;                                // 32 KB: kTerms x rows x 256 B
 constexpr int kOffP = 32768;                            // 2 x 32 KB: kTerms x rows/64 x 16 KB
@@ -84,7 +86,7 @@ constexpr int kOffMax = kOffPs + 8 * kSig;                    // [2][4] floats: 
 constexpr int kOffQMax = kOffMax + 32;                  // bits of the largest |q_rot|
 constexpr int kOffTmem = kOffQMax + 8;
 constexpr int kOffBars = kOffTmem + 8;
-constexpr int kTreeBars = 4 * kRaw + 12 + 1;
+constexpr int kTreeBars = 2 * kRaw + 14 + 1;
 constexpr int kOffPrefix = kOffBars + kTreeBars * 8;
 constexpr int kTcSmem = kOffPrefix + (kMaxBatch + 1) * 4 + 1024;   // + alignment slack
 static_assert(kOffRawK % 16 == 0 && kRawStride % 16 == 0 && kOffBars % 8 == 0 && kOffVis % 16 == 0,
@@ -156,12 +158,6 @@ __device__ __forceinline__ int dim_at(int pos) {
     return (pos & ~7) | ((pos & 1) << 2) | ((pos & 7) >> 1);
 }
 
-// Width of the products for a block of `rows` rows: each warpgroup takes
-// whole chunks of 8, in the counts that soft_segment is compiled for.
-__device__ __forceinline__ int tile_rows(int rows) {
-    return rows <= 64 ? (rows + 15) & ~15 : (rows + 31) & ~31;
-}
-
 // Sum over the warp of 32 values per lane: lane l gets the sum of v[l].
 __device__ __forceinline__ float transpose_sum(float (&v)[32], int lane) {
 #pragma unroll
@@ -214,171 +210,139 @@ struct Soft {
     float c2;                               // log2 logit = S S_k c2
 };
 
-// One tile for kN chunks of 8 rows (chunks wg, wg + 2, ..), in one group or,
-// at eight, in two of four: a group's logits stay in registers between the
-// vote and the weights.  kMasked: the tile holds drafted nodes or ends the
-// sequence; `node` is then this token's node (below 0: context).
+// One tile for kN chunks of 8 rows (chunks wg, wg + 4, ..), whose logits stay
+// in registers between the vote and the weights.  kMasked: the tile holds
+// drafted nodes or ends the sequence; `node` is then this token's node (below
+// 0: context).
 template <int kTerms, int kN, bool kMasked>
 __device__ __forceinline__ void soft_tile(const Soft &c, int it, bool first, int node, int n_nodes,
                                           float (&lp)[8 * kN], bool &ok) {
-    const int b = it & 1;
+    const int b = it & 1, sg = it & (kSig - 1);
     wait_or_fail(ok, c.bx + 8 * (2 + b), (it >> 1) & 1);           // S, and the scales with it
     tc::fence_after_sync();
     const uint32_t q_lane = (uint32_t)(c.t & ~31) << 16;
-    const uint32_t s_col = c.tmem + q_lane + kColS + 128 * b, o_col = c.tmem + q_lane + kColO;
-    const int sg = it & (kSig - 1);
+    const uint32_t s_col = c.tmem + q_lane + kColS + 128 * b + 8 * c.wg;
+    uint32_t r[kN][8];
+    auto load = [&]() {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) tc::tmem_ld8(s_col + 32 * i, r[i]);
+    };
+    load();
     const float skc = ldsf(c.sbase + kOffSig + (kTileT * sg + c.t) * 4) * c.c2;
     const float svp = ldsf(c.sbase + kOffSig + (kTileT * (kSig + sg) + c.t) * 4);
     const float fsv = ldsf(c.sbase + kOffPs + 8 * sg);
     const uint64_t sk2 = pack2(skc, skc), sv2 = pack2(svp, svp);
-    uint32_t see[4] = {};                                          // rows that see this token
-    if constexpr (kMasked) {
+    uint32_t see[kN];                                              // rows that see this token
 #pragma unroll
-        for (int w = 0; w < 4; ++w)
-            see[w] = node < 0 ? 0xFFFFFFFFu
-                   : node < n_nodes ? dmq::lds32(c.sbase + kOffVis + 16 * node + 4 * w) : 0u;
+    for (int i = 0; i < kN; ++i) {
+        see[i] = 0xFFFFFFFFu;
+        if (kMasked && node >= 0)
+            see[i] = node < n_nodes ? dmq::lds32(c.sbase + kOffVis + 16 * node + 4 * i) >> (8 * c.wg) : 0u;
     }
-    auto sees = [&](int i, int k) -> bool {                        // row k of chunk wg + 2 i
-        if constexpr (kMasked)
-            return (see[i >> 1] >> (8 * ((c.wg + 2 * i) & 3) + k)) & 1u;
-        else
-            return true;
-    };
-    const uint32_t pt = c.sbase + kOffP + 32768 * b + c.t * 128;
+    auto sees = [&](int i, int k) -> bool { return !kMasked || ((see[i] >> k) & 1u); };
+    const uint32_t nega = c.sbase + kOffNegM + 32 * c.wg;
+    // log2 p: S skc - m, hidden ones -inf
+    auto logits = [&]() {
+        tc::tmem_wait_ld();
 #pragma unroll
-    for (int i0 = 0; i0 < kN; i0 += kN <= 6 ? kN : 4) {
-        constexpr int kG = kN <= 6 ? kN : 4;
-        const int n = kN - i0 < kG ? kN - i0 : kG;                 // constant once unrolled
-        uint32_t r[kG][8];
-        auto load = [&]() {
-#pragma unroll
-            for (int i = 0; i < kG; ++i)
-                if (i < n) tc::tmem_ld8(s_col + 8 * (c.wg + 2 * (i0 + i)), r[i]);
-            tc::tmem_wait_ld();
-        };
-        // log2 p: S skc - m, hidden ones -inf
-        auto logits = [&]() {
-#pragma unroll
-            for (int i = 0; i < kG; ++i) {
-                if (i >= n) continue;
-                const uint32_t at = c.sbase + kOffNegM + 32 * (c.wg + 2 * (i0 + i));
-                const float4 n0 = lds128f(at), n1 = lds128f(at + 16);
-                const float nm[8] = {n0.x, n0.y, n0.z, n0.w, n1.x, n1.y, n1.z, n1.w};
-#pragma unroll
-                for (int k = 0; k < 8; k += 2) {
-                    float x0, x1;
-                    unpack2(fma2(pack2(__uint_as_float(r[i][k]), __uint_as_float(r[i][k + 1])), sk2,
-                                 pack2(nm[k], nm[k + 1])), x0, x1);
-                    r[i][k] = sees(i0 + i, k) ? __float_as_uint(x0) : 0xFF800000u;
-                    r[i][k + 1] = sees(i0 + i, k + 1) ? __float_as_uint(x1) : 0xFF800000u;
-                }
-            }
-        };
-        load();
-        logits();
-        float top = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < kG; ++i)
-            if (i < n) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) top = fmaxf(top, __uint_as_float(r[i][k]));
-            }
-        if (__builtin_expect(named_or(4 + c.wg, 128, top > kGrow || fsv != 1.f), 0)) {
-            // move the maxima to the tile's, rescale the sums and O: rounds of
-            // four chunks, lane 8 i + k for row k of the round's chunk i
-            constexpr int kRounds = (kG + 3) / 4;
-            load();
-            float keep[kRounds], cc[kRounds], nmx[kRounds];
-#pragma unroll
-            for (int i = 0; i < kG; ++i) {
-                if (i % 4 == 0) keep[i / 4] = kLowest;
-                if (i >= n) continue;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float m = warp_redux_max(
-                        sees(i0 + i, k) ? __uint_as_float(r[i][k]) * skc : -INFINITY);
-                    if (c.lane == 8 * (i % 4) + k) keep[i / 4] = m;
-                }
-            }
-            auto row_of = [&](int round) -> uint32_t {
-                return 8 * (c.wg + 2 * (i0 + 4 * round + (c.lane >> 3))) + (c.lane & 7);
-            };
-            auto in = [&](int round) -> bool { return 4 * round + (c.lane >> 3) < n; };
-            const uint32_t xch = c.sbase + kOffXch, nega = c.sbase + kOffNegM;
-#pragma unroll
-            for (int g = 0; g < kRounds; ++g)
-                if (in(g)) stsf(xch + 512 * (c.t >> 5) + 4 * row_of(g), keep[g]);
-            named_sync(4 + c.wg, 128);
-#pragma unroll
-            for (int g = 0; g < kRounds; ++g) {
-                cc[g] = 1.f;
-                nmx[g] = 0.f;
-                if (!in(g)) continue;
-                const uint32_t at = xch + 4 * row_of(g);
-                const float old = -ldsf(nega + 4 * row_of(g));
-                nmx[g] = fmaxf(fmaxf(fmaxf(ldsf(at), ldsf(at + 512)), fmaxf(ldsf(at + 1024), ldsf(at + 1536))),
-                               old);
-                cc[g] = tc::ex2(old - nmx[g]);
-            }
-            named_sync(4 + c.wg, 128);
-#pragma unroll
-            for (int g = 0; g < kRounds; ++g)
-                if (in(g) && c.t < 32) stsf(nega + 4 * row_of(g), -nmx[g]);
-            if (!first) wait_or_fail(ok, c.bx + 8 * (10 + ((it - 1) & 1)), ((it - 1) >> 1) & 1);
-            tc::fence_after_sync();
-#pragma unroll
-            for (int i = 0; i < kG; ++i) {
-                if (i >= n) continue;
-                uint32_t o[8] = {};
-                const uint32_t col = o_col + 8 * (c.wg + 2 * (i0 + i));
-                if (!first) {
-                    tc::tmem_ld8(col, o);
-                    tc::tmem_wait_ld();
-                }
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float f = __shfl_sync(kFull, cc[i / 4], 8 * (i % 4) + k);
-                    lp[8 * (i0 + i) + k] *= f;
-                    o[k] = __float_as_uint(__uint_as_float(o[k]) * (f * fsv));
-                }
-                if (!first) tc::tmem_st8(col, o);
-            }
-            tc::tmem_wait_st();
-            named_sync(4 + c.wg, 128);                             // the new maxima are in place
-            load();
-            logits();
-        }
-#pragma unroll
-        for (int i = 0; i < kG; ++i) {
-            if (i >= n) continue;
-            const int ch = c.wg + 2 * (i0 + i);
-            float y[8];
+        for (int i = 0; i < kN; ++i) {
+            const float4 n0 = lds128f(nega + 128 * i), n1 = lds128f(nega + 128 * i + 16);
+            const float nm[8] = {n0.x, n0.y, n0.z, n0.w, n1.x, n1.y, n1.z, n1.w};
 #pragma unroll
             for (int k = 0; k < 8; k += 2) {
-                float &l0 = lp[8 * (i0 + i) + k], &l1 = lp[8 * (i0 + i) + k + 1];
-                const uint64_t pr = pack2(tc::ex2(__uint_as_float(r[i][k])),
-                                          tc::ex2(__uint_as_float(r[i][k + 1])));
-                unpack2(add2(pack2(l0, l1), pr), l0, l1);
-                unpack2(mul2(pr, sv2), y[k], y[k + 1]);
-                if constexpr (kMasked) {                           // a hidden block may hold anything
-                    if (!sees(i0 + i, k)) y[k] = 0.f;
-                    if (!sees(i0 + i, k + 1)) y[k + 1] = 0.f;
-                }
+                float x0, x1;
+                unpack2(fma2(pack2(__uint_as_float(r[i][k]), __uint_as_float(r[i][k + 1])), sk2,
+                             pack2(nm[k], nm[k + 1])), x0, x1);
+                r[i][k] = sees(i, k) ? __float_as_uint(x0) : 0xFF800000u;
+                r[i][k + 1] = sees(i, k + 1) ? __float_as_uint(x1) : 0xFF800000u;
             }
-            const uint32_t at = pt + (ch >> 3) * 16384 + (((ch & 7) ^ (c.t & 7)) << 4);
-            uint32_t h[4];
+        }
+    };
+    logits();
+    float top = -INFINITY;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) h[k] = half2_bits(y[2 * k], y[2 * k + 1]);
-            dmq::sts128(at, h[0], h[1], h[2], h[3]);
-            if constexpr (kTerms == 2) {
-                uint32_t lo[4];
+    for (int i = 0; i < kN; ++i)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[k]));
-                    lo[k] = half2_bits(y[2 * k] - f.x, y[2 * k + 1] - f.y);
-                }
-                dmq::sts128(at + 16384, lo[0], lo[1], lo[2], lo[3]);
+        for (int k = 0; k < 8; ++k) top = fmaxf(top, __uint_as_float(r[i][k]));
+    if (__builtin_expect(named_or(4 + c.wg, 128, top > kGrow || fsv != 1.f), 0)) {
+        // move the maxima to the tile's, rescale the sums and O; lane 8 i + k
+        // stands for row k of chunk i
+        load();
+        tc::tmem_wait_ld();
+        float keep = kLowest;
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float m = warp_redux_max(sees(i, k) ? __uint_as_float(r[i][k]) * skc : -INFINITY);
+                if (c.lane == 8 * i + k) keep = m;
             }
+        const uint32_t row = 8 * (c.wg + 4 * (c.lane >> 3)) + (c.lane & 7);
+        const bool mine = c.lane < 8 * kN;
+        const uint32_t xch = c.sbase + kOffXch + 4 * row, neg = c.sbase + kOffNegM + 4 * row;
+        if (mine) stsf(xch + 512 * (c.t >> 5), keep);
+        named_sync(4 + c.wg, 128);
+        float cc = 1.f, nmx = 0.f;
+        if (mine) {
+            const float old = -ldsf(neg);
+            nmx = fmaxf(fmaxf(fmaxf(ldsf(xch), ldsf(xch + 512)), fmaxf(ldsf(xch + 1024), ldsf(xch + 1536))),
+                        old);
+            cc = tc::ex2(old - nmx);
+        }
+        named_sync(4 + c.wg, 128);
+        if (mine && c.t < 32) stsf(neg, -nmx);
+        if (!first) wait_or_fail(ok, c.bx + 8 * (10 + ((it - 1) & 1)), ((it - 1) >> 1) & 1);
+        tc::fence_after_sync();
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            uint32_t o[8] = {};
+            const uint32_t col = c.tmem + q_lane + kColO + 8 * (c.wg + 4 * i);
+            if (!first) {
+                tc::tmem_ld8(col, o);
+                tc::tmem_wait_ld();
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float f = __shfl_sync(kFull, cc, 8 * i + k);
+                lp[8 * i + k] *= f;
+                o[k] = __float_as_uint(__uint_as_float(o[k]) * (f * fsv));
+            }
+            if (!first) tc::tmem_st8(col, o);
+        }
+        tc::tmem_wait_st();
+        named_sync(4 + c.wg, 128);                                 // the new maxima are in place
+        load();
+        logits();
+    }
+    const uint32_t pt = c.sbase + kOffP + 32768 * b + c.t * 128;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+        const int ch = c.wg + 4 * i;
+        float y[8];
+#pragma unroll
+        for (int k = 0; k < 8; k += 2) {
+            float &l0 = lp[8 * i + k], &l1 = lp[8 * i + k + 1];
+            const uint64_t pr = pack2(tc::ex2(__uint_as_float(r[i][k])), tc::ex2(__uint_as_float(r[i][k + 1])));
+            unpack2(add2(pack2(l0, l1), pr), l0, l1);
+            unpack2(mul2(pr, sv2), y[k], y[k + 1]);
+            if constexpr (kMasked) {                               // a hidden block may hold anything
+                if (!sees(i, k)) y[k] = 0.f;
+                if (!sees(i, k + 1)) y[k + 1] = 0.f;
+            }
+        }
+        const uint32_t at = pt + (i >> 1) * 16384 + (((ch & 7) ^ (c.t & 7)) << 4);
+        uint32_t h[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) h[k] = half2_bits(y[2 * k], y[2 * k + 1]);
+        dmq::sts128(at, h[0], h[1], h[2], h[3]);
+        if constexpr (kTerms == 2) {
+            uint32_t lo[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[k]));
+                lo[k] = half2_bits(y[2 * k] - f.x, y[2 * k + 1] - f.y);
+            }
+            dmq::sts128(at + 16384, lo[0], lo[1], lo[2], lo[3]);
         }
     }
     fence_proxy_async();                                           // read by the tensor core
@@ -406,15 +370,23 @@ __device__ __forceinline__ void soft_segment(const Soft &c, int it, int tiles, i
 #pragma unroll 1
     for (; j < tiles; ++j)
         soft_tile<kTerms, kN, true>(c, it + j, j == 0, t0 + j * kTileT + c.t - ctx, n_nodes, lp, ok);
+    float v[32];
 #pragma unroll
-    for (int i0 = 0; i0 < kN; i0 += 4) {
-        float v[32];
-#pragma unroll
-        for (int k = 0; k < 32; ++k) v[k] = 8 * i0 + k < 8 * kN ? lp[8 * i0 + k < 8 * kN ? 8 * i0 + k : 0] : 0.f;
-        const float sum = transpose_sum(v, c.lane);
-        if (i0 + (c.lane >> 3) < kN)
-            stsf(c.sbase + kOffXch + 512 * (c.t >> 5) +
-                     4 * (8 * (c.wg + 2 * (i0 + (c.lane >> 3))) + (c.lane & 7)), sum);
+    for (int k = 0; k < 32; ++k) v[k] = k < 8 * kN ? lp[k < 8 * kN ? k : 0] : 0.f;
+    const float sum = transpose_sum(v, c.lane);
+    if (c.lane < 8 * kN)
+        stsf(c.sbase + kOffXch + 512 * (c.t >> 5) + 4 * (8 * (c.wg + 4 * (c.lane >> 3)) + (c.lane & 7)), sum);
+}
+
+// A warpgroup without rows keeps the hand-offs going.
+__device__ __forceinline__ void soft_idle(const Soft &c, int it, int tiles, bool &ok) {
+#pragma unroll 1
+    for (int j = 0; j < tiles; ++j, ++it) {
+        lazy_or_fail(ok, c.bx + 8 * (2 + (it & 1)), (it >> 1) & 1);
+        if (c.lane == 0) {
+            mbar_arrive(c.bx + 8 * (4 + (it & 1)));
+            mbar_arrive(c.bx + 8 * (8 + (it & 1)));
+        }
     }
 }
 
@@ -436,18 +408,17 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
     const int u0 = share_begin(units, cta, shares), u1 = share_begin(units, cta + 1, shares);
 
     const uint32_t bar0 = sbase + kOffBars;
-    auto kraw_full = [&](int s) { return bar0 + 8 * s; };
-    auto kraw_empty = [&](int s) { return bar0 + 8 * (kRaw + s); };
-    auto vraw_full = [&](int s) { return bar0 + 8 * (2 * kRaw + s); };
-    auto vraw_empty = [&](int s) { return bar0 + 8 * (3 * kRaw + s); };
-    const uint32_t bx = bar0 + 8 * 4 * kRaw;
+    auto raw_full = [&](int s) { return bar0 + 8 * s; };
+    auto raw_empty = [&](int s) { return bar0 + 8 * (kRaw + s); };
+    const uint32_t bx = bar0 + 8 * 2 * kRaw;
     auto k_full = [&](int b) { return bx + 8 * b; };            // K levels -> MMA
     auto s_full = [&](int b) { return bx + 8 * (2 + b); };      // S ready (K levels read)
-    auto s_empty = [&](int b) { return bx + 8 * (4 + b); };     // S and S_k read
+    auto s_empty = [&](int b) { return bx + 8 * (4 + b); };     // S and the scales read
     auto v_full = [&](int b) { return bx + 8 * (6 + b); };      // V levels -> MMA
     auto p_full = [&](int b) { return bx + 8 * (8 + b); };      // P' -> MMA
     auto pv_done = [&](int b) { return bx + 8 * (10 + b); };    // V levels and P' read
-    const uint32_t drained = bx + 8 * 12;
+    auto sig_full = [&](int b) { return bx + 8 * (12 + b); };   // scales -> MMA
+    const uint32_t drained = bx + 8 * 14;
     uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(smem + kOffTmem);
     float *sig_k = reinterpret_cast<float *>(smem + kOffSig);       // [4][128]
     float *sig_v = sig_k + kSig * kTileT;                           // [4][128]
@@ -456,15 +427,12 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
     float *linv = reinterpret_cast<float *>(smem + kOffLinv);
     uint32_t *vis = reinterpret_cast<uint32_t *>(smem + kOffVis);
     float *tps = reinterpret_cast<float *>(smem + kOffPs);
-    float *vmax = reinterpret_cast<float *>(smem + kOffMax);
     uint32_t *qmax = reinterpret_cast<uint32_t *>(smem + kOffQMax);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kRaw; ++s) {
-            mbar_init(kraw_full(s), 1);
-            mbar_init(kraw_empty(s), 4);
-            mbar_init(vraw_full(s), 1);
-            mbar_init(vraw_empty(s), 8);
+            mbar_init(raw_full(s), 1);
+            mbar_init(raw_empty(s), 5);                 // the tile's level warps, the scales
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(k_full(b), 4);
@@ -473,6 +441,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
             mbar_init(v_full(b), 4);
             mbar_init(p_full(b), kSoftWarps);
             mbar_init(pv_done(b), 1);
+            mbar_init(sig_full(b), 1);
         }
         mbar_init(drained, 1);
         *qmax = 0u;
@@ -490,9 +459,9 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
     bool ok = true;                                     // this warp's waits have all come through
     auto wait = [&](uint32_t bar, uint32_t parity) { wait_or_fail(ok, bar, parity); };
     auto lazy = [&](uint32_t bar, uint32_t parity) { lazy_or_fail(ok, bar, parity); };
-    // everyone but the producer and the two idle warps, at the start of a
-    // segment (twice) and at its end
-    auto all_sync = [&]() { named_sync(1, 17 * 32); };
+    // everyone but the producer and the idle warp, at the start of a segment
+    // (twice) and at its end
+    auto all_sync = [&]() { named_sync(1, 26 * 32); };
 
     if (warp < 4) {
         tc::regs_dec<kRegCtl>();
@@ -506,8 +475,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
                 for (int j = 0; j < s.tiles; ++j, ++it) {
                     const int st = it % kRaw;
                     if (it >= kRaw) {
-                        lazy(kraw_empty(st), ((it / kRaw) - 1) & 1);
-                        lazy(vraw_empty(st), ((it / kRaw) - 1) & 1);
+                        lazy(raw_empty(st), ((it / kRaw) - 1) & 1);
                         if (!ok) break;
                     }
                     const int t = (s.tile0 + j) * kTileT;
@@ -515,8 +483,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
                     const int rows = (min(kTileT, stop - t) + 7) & ~7;
                     if (lane == 0) {
                         fence_proxy_async();
-                        mbar_expect_tx(kraw_full(st), (uint32_t)rows * kBlockBytes);
-                        mbar_expect_tx(vraw_full(st), (uint32_t)rows * kBlockBytes);
+                        mbar_expect_tx(raw_full(st), 2u * (uint32_t)rows * kBlockBytes);
                     }
                     __syncwarp();
                     const int r0 = (lane >> 1) * 32;
@@ -525,26 +492,22 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
                         int64_t off = piece_offset(p, s.b, s.g, t + r0);
                         if constexpr (kDebugBounds) off = checked_off(off, nb, p.cache_bytes);
                         const uint32_t to = sbase + st * kRawStride + r0 * kBlockBytes;
-                        if (lane & 1)
-                            bulk_g2s(to + kOffRawV, p.v + off, nb, vraw_full(st));
-                        else
-                            bulk_g2s(to + kOffRawK, p.k + off, nb, kraw_full(st));
+                        bulk_g2s(to + ((lane & 1) ? kOffRawV : kOffRawK), ((lane & 1) ? p.v : p.k) + off,
+                                 nb, raw_full(st));
                     }
                 }
             }
             // after a lost hand-off: the copies still in flight land before the
             // shared memory goes away
-            for (int i = max(0, it - kRaw); i < it; ++i) {
-                mbar_wait_bounded(kraw_full(i % kRaw), (i / kRaw) & 1, kSpinTree);
-                mbar_wait_bounded(vraw_full(i % kRaw), (i / kRaw) & 1, kSpinTree);
-            }
+            for (int i = max(0, it - kRaw); i < it; ++i)
+                mbar_wait_bounded(raw_full(i % kRaw), (i / kRaw) & 1, kSpinTree);
         } else if (warp == 1) {
             // ======================= MMA issuer ==============================
             int it0 = 0;
             for (int u = u0; u < u1;) {
                 const Segment s = segment_at(p, prefix, u, u1);
                 u += s.tiles;
-                const int N = tile_rows(s.rows);
+                const int N = (s.rows + 15) & ~15;
                 const uint32_t idesc_qk = tc::idesc_f16(128, N, false);
                 const uint32_t idesc_pv = tc::idesc_f16(128, N, true);
                 all_sync();
@@ -562,6 +525,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
                     if (jq < s.tiles && jq <= jp + 1) {
                         const int it = it0 + jq, b = it & 1;
                         if (__all_sync(kFull, mbar_test(k_full(b), (it >> 1) & 1) &&
+                                       mbar_test(sig_full(b), (it >> 1) & 1) &&
                                        (it < 2 || mbar_test(s_empty(b), ((it >> 1) - 1) & 1)))) {
                             tc::fence_after_sync();
                             if (leader) {
@@ -620,74 +584,102 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
             mbar_wait_bounded(drained, 0, kSpinTree);
             tc::fence_after_sync();
             tc::tmem_dealloc(tmem, 512);
+        } else if (warp == 2) {
+            // ======================= block scales ============================
+            int it = 0;
+            for (int u = u0; u < u1;) {
+                const Segment s = segment_at(p, prefix, u, u1);
+                u += s.tiles;
+                const int stop = s.ctx + s.n;
+                float ps = 0.f;                         // 0 until a nonzero V scale arrives
+                all_sync();
+                all_sync();
+#pragma unroll 1
+                for (int j = 0; j < s.tiles; ++j, ++it) {
+                    const int st = it % kRaw, b = it & 1, sg = it & (kSig - 1);
+                    wait(raw_full(st), (it / kRaw) & 1);
+                    const uint32_t row = sbase + kOffRawK + st * kRawStride + lane * kBlockBytes;
+                    const int left = stop - (s.tile0 + j) * kTileT - lane;    // tokens from this one on
+                    float sk[4], sv[4], top = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t at = row + 32 * i * kBlockBytes;
+                        sk[i] = half_bits_to_float((uint16_t)dmq::lds16(at));
+                        sv[i] = half_bits_to_float((uint16_t)dmq::lds16(at + kOffRawV - kOffRawK));
+                        if (left <= 32 * i) sv[i] = 0.f;
+                        if (isfinite(sv[i])) top = fmaxf(top, sv[i]);
+                    }
+                    top = warp_redux_max(top);
+                    float f = 1.f;
+                    if (ps == 0.f ? top > 0.f : top * ps > 128.0f) {
+                        const float nps = pow2_floor(__fdividef(128.0f, top));
+                        f = ps == 0.f ? 1.f : pow2_ratio(nps, ps);
+                        ps = nps;
+                    }
+                    // QK(it - 2) was issued after the softmax had read tile it - 4's
+                    if (it >= 2) wait(s_full(b), ((it >> 1) - 1) & 1);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        sig_k[kTileT * sg + 32 * i + lane] = sk[i];
+                        sig_v[kTileT * sg + 32 * i + lane] = sv[i] * ps;
+                    }
+                    if (lane == 0) {
+                        tps[2 * sg] = f;
+                        tps[2 * sg + 1] = ps;
+                    }
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(sig_full(b));
+                        mbar_arrive(raw_empty(st));
+                    }
+                }
+                all_sync();
+            }
         }
-    } else if (warp < 8) {
-        // ======================= K levels ====================================
+    } else if (warp < kSoftWarp0) {
+        // ======================= levels ======================================
         tc::regs_dec<kRegLev>();
-        const int t = threadIdx.x - 4 * 32;             // token of the tile = tensor-memory lane
-        const uint32_t t_lane = tmem + ((uint32_t)(t & ~31) << 16);
-        int it = 0;
+        const int half = (warp >> 2) - 1;               // 0: even tiles, 1: odd ones
+        const int t = threadIdx.x & 127;                // token of the tile = tensor-memory lane
+        const uint32_t k_col = tmem + ((uint32_t)(t & ~31) << 16) + kColK + 64 * half;
+        // 16-byte chunk c of V's row t lies at c ^ (t % 8)
+        const uint32_t v_row = sbase + kOffV + 32768 * half + t * 128 + ((t & 7) << 4);
+        int it0 = 0;
         for (int u = u0; u < u1;) {
             const Segment s = segment_at(p, prefix, u, u1);
             u += s.tiles;
-            // rows of the block that see node j, one bit each: lane = row 32 w +
-            // lane with its node's mask, a vote per node
-            {
+            if (half == 0) {
+                // rows of the block that see node j, one bit each: lane = row
+                // 32 w + lane with its node's mask, a vote per node
                 const int w = warp & 3, c = 32 * w + lane;
                 unsigned long long m = 0ull;
                 if (c < s.rows) m = __ldg(p.mask + s.b * p.mask_stride + (s.row0 + c) / p.G);
 #pragma unroll 1
                 for (int jh = 0; jh < 2; ++jh) {
-                    const uint32_t half = (uint32_t)(m >> (32 * jh));
+                    const uint32_t bits = (uint32_t)(m >> (32 * jh));
                     uint32_t mine = 0;
 #pragma unroll 8
                     for (int k = 0; k < 32; ++k) {
-                        const uint32_t v = __ballot_sync(kFull, (half >> k) & 1u);
+                        const uint32_t v = __ballot_sync(kFull, (bits >> k) & 1u);
                         if (lane == k) mine = v;
                     }
                     vis[4 * (32 * jh + lane) + w] = mine;
                 }
             }
-            const int stop = s.ctx + s.n;
-            float ps = 0.f;                             // 0 until a nonzero V scale arrives
             all_sync();
             all_sync();
-            for (int j = 0; j < s.tiles; ++j, ++it) {
-                const int st = it % kRaw, b = it & 1;
-                wait(kraw_full(st), (it / kRaw) & 1);
-                wait(vraw_full(st), (it / kRaw) & 1);
-                const uint32_t row = sbase + kOffRawK + st * kRawStride + t * kBlockBytes;
-                const float sk = half_bits_to_float((uint16_t)dmq::lds16(row));
-                const float sv = (s.tile0 + j) * kTileT + t < stop
-                    ? half_bits_to_float((uint16_t)dmq::lds16(row + kOffRawV - kOffRawK)) : 0.f;
-                // the tile's largest finite V scale
-                const float mine = warp_redux_max(isfinite(sv) ? sv : 0.f);
-                if (lane == 0) vmax[4 * b + (warp & 3)] = mine;
-                // the row's words, four ahead of their use
-                const uint32_t a0 = (row + 2) & ~3u, sh = ((row + 2) & 3u) * 8u;
+#pragma unroll 1
+            for (int it = it0 + ((it0 ^ half) & 1); it < it0 + s.tiles; it += 2) {
+                const int st = it % kRaw;
+                const uint32_t before = ((it >> 1) - 1) & 1;
+                wait(raw_full(st), (it / kRaw) & 1);
+                const uint32_t row = sbase + kOffRawK + st * kRawStride + t * kBlockBytes + 2;
+                const uint32_t a0 = row & ~3u, sh = (row & 3u) * 8u;
+                if (it >= 2) wait(s_full(half), before);            // QK(it - 2) has read this buffer
+                tc::fence_after_sync();
                 uint32_t w[5];
 #pragma unroll
                 for (int i = 0; i < 5; ++i) w[i] = dmq::lds32(a0 + 4 * i);
-                named_sync(2, 128);
-                const float4 m4 = *reinterpret_cast<const float4 *>(vmax + 4 * b);
-                const float top = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
-                float f = 1.f;
-                if (ps == 0.f ? top > 0.f : top * ps > 128.0f) {
-                    const float nps = pow2_floor(__fdividef(128.0f, top));
-                    f = ps == 0.f ? 1.f : pow2_ratio(nps, ps);
-                    ps = nps;
-                }
-                // QK(it - 2) has read this K buffer, and was issued after the
-                // softmax had read tile it - 4's scales
-                if (it >= 2) wait(s_full(b), ((it >> 1) - 1) & 1);
-                tc::fence_after_sync();
-                const int sg = it & (kSig - 1);
-                sig_k[kTileT * sg + t] = sk;
-                sig_v[kTileT * sg + t] = sv * ps;
-                if (t == 0) {
-                    tps[2 * sg] = f;
-                    tps[2 * sg + 1] = ps;
-                }
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {           // four words: 32 levels, 16 columns
                     uint32_t o[16], nx[4];
@@ -700,54 +692,30 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) o[4 * i + e] = l[e];
                     }
-                    tc::tmem_st16(t_lane + kColK + 64 * b + 16 * c, o);
+                    tc::tmem_st16(k_col + 16 * c, o);
                     w[0] = w[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) w[i + 1] = nx[i];
                 }
+                const uint32_t v0 = a0 + kOffRawV - kOffRawK;
+#pragma unroll
+                for (int i = 0; i < 5; ++i) w[i] = dmq::lds32(v0 + 4 * i);
                 tc::tmem_wait_st();
                 tc::fence_before_sync();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(k_full(b));
-                    mbar_arrive(kraw_empty(st));
-                    mbar_arrive(vraw_empty(st));
-                }
-            }
-            all_sync();
-        }
-    } else if (warp < kSoftWarp0) {
-        // ======================= V levels ====================================
-        tc::regs_dec<kRegLev>();
-        const int t = threadIdx.x - 8 * 32;             // token of the tile
-        int it = 0;
-        for (int u = u0; u < u1;) {
-            const Segment s = segment_at(p, prefix, u, u1);
-            u += s.tiles;
-            all_sync();
-            all_sync();
-            for (int j = 0; j < s.tiles; ++j, ++it) {
-                const int st = it % kRaw, b = it & 1;
-                wait(vraw_full(st), (it / kRaw) & 1);
-                const uint32_t row = sbase + kOffRawV + st * kRawStride + t * kBlockBytes;
-                const uint32_t a0 = (row + 2) & ~3u, sh = ((row + 2) & 3u) * 8u;
-                uint32_t w[5];
-#pragma unroll
-                for (int i = 0; i < 5; ++i) w[i] = dmq::lds32(a0 + 4 * i);
-                if (it >= 2) wait(pv_done(b), ((it >> 1) - 1) & 1);
-                // 16-byte chunk c of row t lies at c ^ (t % 8)
-                const uint32_t to = sbase + kOffV + 32768 * b + t * 128 + ((t & 7) << 4);
+                if (lane == 0) mbar_arrive(k_full(half));
+                if (it >= 2) wait(pv_done(half), before);
 #pragma unroll 1
                 for (int c = 0; c < 16; c += 4) {       // a word: eight levels, 16 bytes
                     uint32_t nx[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) nx[i] = dmq::lds32(a0 + 4 * min(c + 5 + i, 16));
-                    const uint32_t tc4 = (to ^ ((c & 4) << 4)) + (c >> 3) * 16384;
+                    for (int i = 0; i < 4; ++i) nx[i] = dmq::lds32(v0 + 4 * min(c + 5 + i, 16));
+                    const uint32_t to = (v_row ^ ((c & 4) << 4)) + (c >> 3) * 16384;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         uint32_t l[4];
                         word_levels(__funnelshift_r(w[i], w[i + 1], sh), l);
-                        dmq::sts128(tc4 ^ (i << 4), l[0], l[1], l[2], l[3]);
+                        dmq::sts128(to ^ (i << 4), l[0], l[1], l[2], l[3]);
                     }
                     w[0] = w[4];
 #pragma unroll
@@ -756,10 +724,11 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
                 fence_proxy_async();                    // read by the tensor core
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(v_full(b));
-                    mbar_arrive(vraw_empty(st));
+                    mbar_arrive(v_full(half));
+                    mbar_arrive(raw_empty(st));
                 }
             }
+            it0 += s.tiles;
             all_sync();
         }
     } else {
@@ -775,7 +744,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
             const Segment s = segment_at(p, prefix, u, u1);
             const bool whole = s.tiles == s.work_tiles;
             u += s.tiles;
-            const int N = tile_rows(s.rows), nch = N >> 3;
+            const int N = (s.rows + 15) & ~15, nch = N >> 3;
             // ---- queries: rotate, agree on the power of two, store -----------
             // (rolled loops through shared memory: straight-line code that runs
             // once per segment costs its instruction fetches, some 25 us at 16
@@ -854,17 +823,16 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
 
             const Soft sc = {sbase, tmem, bx, t, lane, wg, c2};
             const int t0 = s.tile0 * kTileT;
-            switch (N >> 4) {                           // chunks of this warpgroup
+            switch ((nch - wg + 3) >> 2) {              // chunks of this warpgroup
+                case 0: soft_idle(sc, it, s.tiles, ok); break;
                 case 1: soft_segment<kTerms, 1>(sc, it, s.tiles, t0, s.ctx, s.n, ok); break;
                 case 2: soft_segment<kTerms, 2>(sc, it, s.tiles, t0, s.ctx, s.n, ok); break;
-                case 3: soft_segment<kTerms, 3>(sc, it, s.tiles, t0, s.ctx, s.n, ok); break;
-                case 4: soft_segment<kTerms, 4>(sc, it, s.tiles, t0, s.ctx, s.n, ok); break;
                 default:
                     if constexpr (kTerms == 1) {
-                        if (N <= 96)
-                            soft_segment<kTerms, 6>(sc, it, s.tiles, t0, s.ctx, s.n, ok);
+                        if (nch - wg <= 12)
+                            soft_segment<kTerms, 3>(sc, it, s.tiles, t0, s.ctx, s.n, ok);
                         else
-                            soft_segment<kTerms, 8>(sc, it, s.tiles, t0, s.ctx, s.n, ok);
+                            soft_segment<kTerms, 4>(sc, it, s.tiles, t0, s.ctx, s.n, ok);
                     }
             }
             it += s.tiles;
@@ -877,9 +845,8 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
             // sum_t P'_t (2n - 15) 2^-11 -> sum_t p S_v (2n - 15) / 15
             const float back = (ps > 0.f ? pow2_inv(ps) : 1.0f) * (2048.0f / 15.0f);
             named_sync(wg_bar, 128);
-            for (int r = t; r < 64; r += 128) {
-                const int row = 8 * (wg + 2 * (r >> 3)) + (r & 7);
-                if (row >= s.rows) break;
+            const int row = 8 * (wg + 4 * (t >> 3)) + (t & 7);
+            if (t < 32 && row < s.rows) {
                 const float L = (xch[row] + xch[128 + row]) + (xch[256 + row] + xch[384 + row]);
                 if (whole)
                     linv[row] = L == 0.f ? 0.f : 1.0f / L;
@@ -889,7 +856,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
             const int d = dim_at(t);
             float *po = p.part_o + (int64_t)part_slot(s, cta) * p.rows * kD;
 #pragma unroll 1
-            for (int c = wg; c < nch; c += 2) {          // (V is done with its buffers)
+            for (int c = wg; c < nch; c += 4) {          // (V is done with its buffers)
                 uint32_t o[8];
                 tc::tmem_ld8(t_lane + kColO + 8 * c, o);
                 tc::tmem_wait_ld();
