@@ -52,6 +52,7 @@ struct TreeParams {
     float *part_o;                          // [2 n_ctas][rows][128]
     float2 *part_ml;                        // [2 n_ctas][rows]: max (log2 units), sum
     int n_ctas;
+    int join_starts;                        // how tree_combine_kernel finds the split works
     void *out;                              // [B][T][Hq][128]
     int out_type;
     int64_t cache_bytes, out_elems;         // extents, for the debug build's bounds checks
@@ -174,14 +175,18 @@ __device__ __forceinline__ void store_out(const TreeParams &p, int b, int g, int
     if (in_extent(oi, 4, p.out_elems)) store4(p.out, p.out_type, oi, v);
 }
 
-// Joins the works that cross CTAs.  grid.x walks the starts of shares 1 .. : a
-// start that lies inside a work, and is the first such start, owns the work.
+// Joins the works that cross CTAs.  Few works: grid.x numbers them (sequence,
+// KV head, row block).  More works than shares (p.join_starts): grid.x walks
+// the starts of shares 1 .. instead; a start that lies inside a work, and is
+// the first such start, owns the work.  Either way at most one CTA column per
+// split work does anything (walking the starts of 148 shares for the four
+// works of one sequence took 17 to 39 us, mostly CTAs that found nothing).
 // Four warps per row take every fourth partial with a running maximum, and
 // the four results meet in shared memory.
 constexpr int kJoinWarps = 4, kJoinRows = 4;
 
 __global__ void __launch_bounds__(kJoinWarps * kJoinRows * 32)
-tree_combine_kernel(const TreeParams p) {
+tree_combine_kernel(const __grid_constant__ TreeParams p) {
     __shared__ int prefix[kMaxBatch + 1];
     __shared__ float4 o_s[kJoinRows][kJoinWarps][32];
     __shared__ float2 ml_s[kJoinRows][kJoinWarps];
@@ -190,16 +195,30 @@ tree_combine_kernel(const TreeParams p) {
     // this one may start once this grid has ended
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int units = prefix[p.B], shares = n_shares(p, units);
-    const int c1 = blockIdx.x + 1;
-    if (c1 >= shares) return;
-    const int u = share_begin(units, c1, shares);
+    int u;                                  // a unit of the work
+    if (p.join_starts) {
+        const int c1 = blockIdx.x + 1;
+        if (c1 >= shares) return;
+        u = share_begin(units, c1, shares);
+    } else {
+        const int most = (p.T * p.G + p.rows - 1) / p.rows;        // blocks of a sequence, at most
+        const int blk = blockIdx.x % most, bg = blockIdx.x / most;
+        const int b = bg / p.Hkv, g = bg - b * p.Hkv;
+        int ctx, n;
+        seq_extent(p, b, ctx, n);
+        const int blocks = seq_blocks(p, n);
+        if (blk >= blocks) return;
+        u = prefix[b] + (g * blocks + blk) * seq_tiles(ctx, n);
+    }
     const Segment s = segment_at(p, prefix, u, units);
     const int first = share_of(units, s.begin, shares);
     const int last = share_of(units, s.begin + s.work_tiles - 1, shares);
+    if (first == last) return;              // whole: its CTA wrote the rows
+    if (p.join_starts && (u == s.begin || first != (int)blockIdx.x)) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int sub = warp % kJoinWarps, ri = warp / kJoinWarps;
     const int r = blockIdx.y * kJoinRows + ri;
-    if (u == s.begin || first != c1 - 1 || (int)blockIdx.y * kJoinRows >= s.rows) return;
+    if ((int)blockIdx.y * kJoinRows >= s.rows) return;
     float M = -INFINITY, L = 0.f;
     float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r < s.rows) {

@@ -817,6 +817,8 @@ tbq4_status tree_impl(const void *q, int q_dtype, const uint8_t *k, const uint8_
     p.scale = softmax_scale;
     sign_words(sign_seed, &p.sign_lo, &p.sign_hi);
     p.n_ctas = kNumSMs;
+    const int64_t works = (int64_t)B * Hkv * ceil_div((int64_t)T * p.G, rows);
+    p.join_starts = works >= p.n_ctas;
     p.part_o = static_cast<float *>(workspace);
     p.part_ml = reinterpret_cast<float2 *>(p.part_o + (size_t)2 * p.n_ctas * rows * kD);
     p.out = out;
@@ -842,10 +844,10 @@ tbq4_status tree_impl(const void *q, int q_dtype, const uint8_t *k, const uint8_
         tree::tree_tc_kernel<2><<<p.n_ctas, tree::kTcThreads, tree::kTcSmem, st>>>(p);
     else
         tree::tree_tc_kernel<1><<<p.n_ctas, tree::kTcThreads, tree::kTcSmem, st>>>(p);
-    // the join, a programmatic dependent launch: one CTA per start of a share
-    // and group of rows
+    // the join, a programmatic dependent launch: one CTA per work (or start of
+    // a share, when there are more works than shares) and group of rows
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.n_ctas - 1,
+    cfg.gridDim = dim3((unsigned)(p.join_starts ? p.n_ctas - 1 : works),
                        (unsigned)ceil_div(std::min(rows, T * p.G), tree::kJoinRows));
     cfg.blockDim = dim3(tree::kJoinWarps * tree::kJoinRows * 32);
     cfg.stream = st;
