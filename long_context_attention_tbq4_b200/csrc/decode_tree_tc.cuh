@@ -33,14 +33,14 @@
 // running maximum is one number for all threads (shared memory).  The
 // maximum moves only when a logit exceeds it by 8 in log2 units: one
 // barrier-with-vote per warpgroup and tile decides that, and the rare path
-// takes the tile's maxima and rescales O.  Sums stay in registers until the
-// end.  Tiles that hold drafted nodes or the end of the sequence apply masks
+// takes the tile's maxima and rescales O (see soft_tile).  Sums stay in
+// registers until the end.  Tiles that hold drafted nodes or the end of the sequence apply masks
 // by select, to logits and to weights (a hidden block may hold anything).
 //
 // Warps (28): 0 producer (cp.async.bulk, 32-token pieces), 1 tensor-memory
 // allocation and every tcgen05.mma, 2 block scales, 4-7 and 8-11 levels (K
-// and V of the even and of the odd tiles), 12-27 softmax (four warpgroups;
-// 8-row chunk c belongs to warpgroup c % 4).  Every role is bound by latency
+// and V of the even and of the odd tiles), 12-27 softmax (four warpgroups
+// of 32 rows each; those without rows sleep until the block is done).  Every role is bound by latency
 // rather than by a unit, hence that many warps and the two level groups.
 // The softmax waits for one barrier per tile: QK(j) is issued once levels and
 // scales of tile j are there, and its commit covers PV(j - 2), which read the
@@ -67,7 +67,7 @@ constexpr float kLowest = -1e30f;                       // running maximum befor
 // registers per thread by warpgroup: control, levels (2), softmax (4)
 // (setmaxnreg draws on what the block was launched with: the host refuses to
 // launch a build that compiled to fewer than kLaunchRegs)
-constexpr uint32_t kRegCtl = 40, kRegLev = 40, kRegSoft = 96;
+constexpr uint32_t kRegCtl = 56, kRegLev = 48, kRegSoft = 88;
 constexpr int kLaunchRegs = 72;
 static_assert(4 * kRegCtl + 8 * kRegLev + 16 * kRegSoft <= 28 * kLaunchRegs, "register split");
 
@@ -86,7 +86,7 @@ constexpr int kOffMax = kOffPs + 8 * kSig;                    // [2][4] floats: 
 constexpr int kOffQMax = kOffMax + 32;                  // bits of the largest |q_rot|
 constexpr int kOffTmem = kOffQMax + 8;
 constexpr int kOffBars = kOffTmem + 8;
-constexpr int kTreeBars = 2 * kRaw + 14 + 1;
+constexpr int kTreeBars = 2 * kRaw + 12 + 1;
 constexpr int kOffPrefix = kOffBars + kTreeBars * 8;
 constexpr int kTcSmem = kOffPrefix + (kMaxBatch + 1) * 4 + 1024;   // + alignment slack
 static_assert(kOffRawK % 16 == 0 && kRawStride % 16 == 0 && kOffBars % 8 == 0 && kOffVis % 16 == 0,
@@ -183,21 +183,29 @@ __device__ __forceinline__ void stsf(uint32_t a, float x) {
     asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(x) : "memory");
 }
 
-// Bounded wait of one warp: false once one has run out, and from then on at
-// once (the error is recorded the first time).
-__device__ __forceinline__ void wait_or_fail(bool &ok, uint32_t bar, uint32_t parity) {
-    if (ok && !mbar_wait_bounded(bar, parity, kSpinTree)) {
-        ok = false;
-        record_status(7u /* TBQ4_ERR_DEVICE_TIMEOUT */);
-    }
+// Arrivals that complete a P' tile: each of the 4 n warps of the n
+// warpgroups with rows counts 12 / n.
+constexpr uint32_t kPArrivals = 48;
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
 
-// The same for the warps that run ahead of the softmax: they sleep between
-// polls, which leaves the schedulers to it (tight polling by the level and
-// copy warps was a quarter of all instructions).
-constexpr uint32_t kLazyTree = 64;                      // nanoseconds
-__device__ __forceinline__ void lazy_or_fail(bool &ok, uint32_t bar, uint32_t parity) {
-    if (ok && !mbar_wait_lazy_warp(bar, parity, kSpinTree, kLazyTree)) {
+// Bounded wait of one warp: false once one has run out, and from then on at
+// once (the error is recorded the first time).  Each poll suspends the warp
+// for up to kPollNs, or returns when the phase completes.
+constexpr uint32_t kPolls = 1u << 20, kPollNs = 2000;
+__device__ __forceinline__ void wait_or_fail(bool &ok, uint32_t bar, uint32_t parity) {
+    if (!ok) return;
+    uint32_t left;
+    asm volatile(
+        "{\n .reg .pred p;\n mov.u32 %0, %3;\n"
+        "WAIT:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %4;\n"
+        " @p bra DONE;\n sub.u32 %0, %0, 1;\n setp.ne.u32 p, %0, 0;\n @p bra WAIT;\n"
+        "DONE:\n}\n"
+        : "=&r"(left)
+        : "r"(bar), "r"(parity), "n"(kPolls), "r"(kPollNs)
+        : "memory");
+    if (!__all_sync(kFull, left != 0)) {
         ok = false;
         record_status(7u /* TBQ4_ERR_DEVICE_TIMEOUT */);
     }
@@ -207,13 +215,20 @@ __device__ __forceinline__ void lazy_or_fail(bool &ok, uint32_t bar, uint32_t pa
 struct Soft {
     uint32_t sbase, tmem, bx;               // shared memory, tensor memory, first hand-off barrier
     int t, lane, wg;                        // token of the tile, lane, warpgroup
+    uint32_t weight;                        // what its arrival counts (kPArrivals)
     float c2;                               // log2 logit = S S_k c2
 };
 
-// One tile for kN chunks of 8 rows (chunks wg, wg + 4, ..), whose logits stay
-// in registers between the vote and the weights.  kMasked: the tile holds
-// drafted nodes or ends the sequence; `node` is then this token's node (below
-// 0: context).
+// One tile for kN chunks of 8 rows (rows 32 wg + 8 i ..).  The weights are
+// taken with the running maxima as they are, stored, and only then does the
+// warpgroup vote on whether a logit exceeded its maximum by more than kGrow
+// (a weight above 2^8, which fp16 may not hold): the rare tile that did is
+// stored again with the new maxima.  The sums take that without a second
+// pass: fp32 holds weights of up to 2^127, so they are scaled afterwards, and
+// where a maximum rose by more than 64 the old sum no longer counts.  (Voting
+// first kept 32 logits a thread in registers across the barrier and spilled.)
+// kMasked: the tile holds drafted nodes or ends the sequence; `node` is then
+// this token's node (below 0: context).
 template <int kTerms, int kN, bool kMasked>
 __device__ __forceinline__ void soft_tile(const Soft &c, int it, bool first, int node, int n_nodes,
                                           float (&lp)[8 * kN], bool &ok) {
@@ -221,116 +236,30 @@ __device__ __forceinline__ void soft_tile(const Soft &c, int it, bool first, int
     wait_or_fail(ok, c.bx + 8 * (2 + b), (it >> 1) & 1);           // S, and the scales with it
     tc::fence_after_sync();
     const uint32_t q_lane = (uint32_t)(c.t & ~31) << 16;
-    const uint32_t s_col = c.tmem + q_lane + kColS + 128 * b + 8 * c.wg;
-    uint32_t r[kN][8];
-    auto load = [&]() {
-#pragma unroll
-        for (int i = 0; i < kN; ++i) tc::tmem_ld8(s_col + 32 * i, r[i]);
-    };
-    load();
+    const uint32_t s_col = c.tmem + q_lane + kColS + 128 * b + 32 * c.wg;
     const float skc = ldsf(c.sbase + kOffSig + (kTileT * sg + c.t) * 4) * c.c2;
     const float svp = ldsf(c.sbase + kOffSig + (kTileT * (kSig + sg) + c.t) * 4);
     const float fsv = ldsf(c.sbase + kOffPs + 8 * sg);
-    const uint64_t sk2 = pack2(skc, skc), sv2 = pack2(svp, svp);
-    uint32_t see[kN];                                              // rows that see this token
-#pragma unroll
-    for (int i = 0; i < kN; ++i) {
-        see[i] = 0xFFFFFFFFu;
-        if (kMasked && node >= 0)
-            see[i] = node < n_nodes ? dmq::lds32(c.sbase + kOffVis + 16 * node + 4 * i) >> (8 * c.wg) : 0u;
-    }
-    auto sees = [&](int i, int k) -> bool { return !kMasked || ((see[i] >> k) & 1u); };
-    const uint32_t nega = c.sbase + kOffNegM + 32 * c.wg;
-    // log2 p: S skc - m, hidden ones -inf
-    auto logits = [&]() {
-        tc::tmem_wait_ld();
-#pragma unroll
-        for (int i = 0; i < kN; ++i) {
-            const float4 n0 = lds128f(nega + 128 * i), n1 = lds128f(nega + 128 * i + 16);
-            const float nm[8] = {n0.x, n0.y, n0.z, n0.w, n1.x, n1.y, n1.z, n1.w};
-#pragma unroll
-            for (int k = 0; k < 8; k += 2) {
-                float x0, x1;
-                unpack2(fma2(pack2(__uint_as_float(r[i][k]), __uint_as_float(r[i][k + 1])), sk2,
-                             pack2(nm[k], nm[k + 1])), x0, x1);
-                r[i][k] = sees(i, k) ? __float_as_uint(x0) : 0xFF800000u;
-                r[i][k + 1] = sees(i, k + 1) ? __float_as_uint(x1) : 0xFF800000u;
-            }
-        }
-    };
-    logits();
-    float top = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < kN; ++i)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) top = fmaxf(top, __uint_as_float(r[i][k]));
-    if (__builtin_expect(named_or(4 + c.wg, 128, top > kGrow || fsv != 1.f), 0)) {
-        // move the maxima to the tile's, rescale the sums and O; lane 8 i + k
-        // stands for row k of chunk i
-        load();
-        tc::tmem_wait_ld();
-        float keep = kLowest;
-#pragma unroll
-        for (int i = 0; i < kN; ++i)
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float m = warp_redux_max(sees(i, k) ? __uint_as_float(r[i][k]) * skc : -INFINITY);
-                if (c.lane == 8 * i + k) keep = m;
-            }
-        const uint32_t row = 8 * (c.wg + 4 * (c.lane >> 3)) + (c.lane & 7);
-        const bool mine = c.lane < 8 * kN;
-        const uint32_t xch = c.sbase + kOffXch + 4 * row, neg = c.sbase + kOffNegM + 4 * row;
-        if (mine) stsf(xch + 512 * (c.t >> 5), keep);
-        named_sync(4 + c.wg, 128);
-        float cc = 1.f, nmx = 0.f;
-        if (mine) {
-            const float old = -ldsf(neg);
-            nmx = fmaxf(fmaxf(fmaxf(ldsf(xch), ldsf(xch + 512)), fmaxf(ldsf(xch + 1024), ldsf(xch + 1536))),
-                        old);
-            cc = tc::ex2(old - nmx);
-        }
-        named_sync(4 + c.wg, 128);
-        if (mine && c.t < 32) stsf(neg, -nmx);
-        if (!first) wait_or_fail(ok, c.bx + 8 * (10 + ((it - 1) & 1)), ((it - 1) >> 1) & 1);
-        tc::fence_after_sync();
-#pragma unroll
-        for (int i = 0; i < kN; ++i) {
-            uint32_t o[8] = {};
-            const uint32_t col = c.tmem + q_lane + kColO + 8 * (c.wg + 4 * i);
-            if (!first) {
-                tc::tmem_ld8(col, o);
-                tc::tmem_wait_ld();
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float f = __shfl_sync(kFull, cc, 8 * i + k);
-                lp[8 * i + k] *= f;
-                o[k] = __float_as_uint(__uint_as_float(o[k]) * (f * fsv));
-            }
-            if (!first) tc::tmem_st8(col, o);
-        }
-        tc::tmem_wait_st();
-        named_sync(4 + c.wg, 128);                                 // the new maxima are in place
-        load();
-        logits();
-    }
-    const uint32_t pt = c.sbase + kOffP + 32768 * b + c.t * 128;
-#pragma unroll
-    for (int i = 0; i < kN; ++i) {
-        const int ch = c.wg + 4 * i;
+    uint32_t see = 0xFFFFFFFFu;                                    // rows that see this token
+    if (kMasked && node >= 0)
+        see = node < n_nodes ? dmq::lds32(c.sbase + kOffVis + 16 * node + 4 * c.wg) : 0u;
+    auto sees = [&](int i, int k) -> bool { return !kMasked || ((see >> (8 * i + k)) & 1u); };
+    // 16-byte chunk x of a P' row lies at x ^ (t % 8); this warpgroup's are
+    // 4 (wg % 2) + i of the 64-row atom wg / 2
+    const uint32_t pt = c.sbase + kOffP + 32768 * b + (c.wg >> 1) * 16384 + c.t * 128 +
+                        ((((c.wg & 1) << 2) ^ (c.t & 7)) << 4);
+    // P' = p S_v ps of chunk i
+    auto store = [&](int i, const float (&pr)[8]) {
         float y[8];
 #pragma unroll
         for (int k = 0; k < 8; k += 2) {
-            float &l0 = lp[8 * i + k], &l1 = lp[8 * i + k + 1];
-            const uint64_t pr = pack2(tc::ex2(__uint_as_float(r[i][k])), tc::ex2(__uint_as_float(r[i][k + 1])));
-            unpack2(add2(pack2(l0, l1), pr), l0, l1);
-            unpack2(mul2(pr, sv2), y[k], y[k + 1]);
+            unpack2(mul2(pack2(pr[k], pr[k + 1]), pack2(svp, svp)), y[k], y[k + 1]);
             if constexpr (kMasked) {                               // a hidden block may hold anything
                 if (!sees(i, k)) y[k] = 0.f;
                 if (!sees(i, k + 1)) y[k + 1] = 0.f;
             }
         }
-        const uint32_t at = pt + (i >> 1) * 16384 + (((ch & 7) ^ (c.t & 7)) << 4);
+        const uint32_t at = pt ^ (i << 4);
         uint32_t h[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) h[k] = half2_bits(y[2 * k], y[2 * k + 1]);
@@ -344,14 +273,96 @@ __device__ __forceinline__ void soft_tile(const Soft &c, int it, bool first, int
             }
             dmq::sts128(at + 16384, lo[0], lo[1], lo[2], lo[3]);
         }
+    };
+    float top = -INFINITY;
+#pragma unroll
+    for (int i0 = 0; i0 < kN; i0 += 2) {
+        uint32_t r[2][8];
+        tc::tmem_ld8(s_col + 8 * i0, r[0]);
+        tc::tmem_ld8(s_col + 8 * i0 + 8, r[1]);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int i = i0 + e;
+            const uint32_t nega = c.sbase + kOffNegM + 128 * c.wg + 32 * i;
+            const float4 n0 = lds128f(nega), n1 = lds128f(nega + 16);
+            const float nm[8] = {n0.x, n0.y, n0.z, n0.w, n1.x, n1.y, n1.z, n1.w};
+            float x[8];                                            // log2 p: S skc - m, hidden ones -inf
+#pragma unroll
+            for (int k = 0; k < 8; k += 2) {
+                unpack2(fma2(pack2(__uint_as_float(r[e][k]), __uint_as_float(r[e][k + 1])),
+                             pack2(skc, skc), pack2(nm[k], nm[k + 1])), x[k], x[k + 1]);
+                if (!sees(i, k)) x[k] = -INFINITY;
+                if (!sees(i, k + 1)) x[k + 1] = -INFINITY;
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) top = fmaxf(top, x[k]);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = tc::ex2(x[k]);
+#pragma unroll
+            for (int k = 0; k < 8; k += 2)
+                unpack2(add2(pack2(lp[8 * i + k], lp[8 * i + k + 1]), pack2(x[k], x[k + 1])),
+                        lp[8 * i + k], lp[8 * i + k + 1]);
+            store(i, x);
+        }
+    }
+    if (__builtin_expect(named_or(4 + c.wg, 128, top > kGrow || fsv != 1.f), 0)) {
+        // move the maxima to the tile's; lane 8 i + k stands for row k of chunk i
+        float keep = kLowest;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            uint32_t r[8];
+            tc::tmem_ld8(s_col + 8 * i, r);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float m = warp_redux_max(sees(i, k) ? __uint_as_float(r[k]) * skc : -INFINITY);
+                if (c.lane == 8 * i + k) keep = m;
+            }
+        }
+        const uint32_t row = 32 * c.wg + c.lane;
+        const bool mine = c.lane < 8 * kN;
+        const uint32_t xch = c.sbase + kOffXch + 4 * row, neg = c.sbase + kOffNegM + 4 * row;
+        if (mine) stsf(xch + 512 * (c.t >> 5), keep);
+        named_sync(4 + c.wg, 128);
+        float rise = 0.f, nmx = 0.f;
+        if (mine) {
+            const float old = -ldsf(neg);
+            nmx = fmaxf(fmaxf(fmaxf(ldsf(xch), ldsf(xch + 512)), fmaxf(ldsf(xch + 1024), ldsf(xch + 1536))),
+                        old);
+            rise = nmx - old;
+        }
+        named_sync(4 + c.wg, 128);
+        if (mine && c.t < 32) stsf(neg, -nmx);
+        if (!first) wait_or_fail(ok, c.bx + 8 * (8 + ((it - 1) & 1)), ((it - 1) >> 1) & 1);
+        tc::fence_after_sync();
+        // this token's weights once more, the sums and O by 2^-rise
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            uint32_t r[8], o[8] = {};
+            const uint32_t col = c.tmem + q_lane + kColO + 32 * c.wg + 8 * i;
+            tc::tmem_ld8(s_col + 8 * i, r);
+            if (!first) tc::tmem_ld8(col, o);
+            tc::tmem_wait_ld();
+            float x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float up = __shfl_sync(kFull, rise, 8 * i + k), f = tc::ex2(-up);
+                const float m = __shfl_sync(kFull, nmx, 8 * i + k);
+                x[k] = sees(i, k) ? tc::ex2(fmaf(__uint_as_float(r[k]), skc, -m)) : 0.f;
+                lp[8 * i + k] = up > 64.0f ? x[k] : lp[8 * i + k] * f;
+                o[k] = __float_as_uint(__uint_as_float(o[k]) * (f * fsv));
+            }
+            if (!first) tc::tmem_st8(col, o);
+            store(i, x);
+        }
+        tc::tmem_wait_st();
+        named_sync(4 + c.wg, 128);                                 // the new maxima are in place
     }
     fence_proxy_async();                                           // read by the tensor core
     tc::fence_before_sync();
     __syncwarp();
-    if (c.lane == 0) {
-        mbar_arrive(c.bx + 8 * (4 + b));                           // S and the scales are read
-        mbar_arrive(c.bx + 8 * (8 + b));                           // P' is written
-    }
+    if (c.lane == 0) mbar_arrive_n(c.bx + 8 * (4 + b), c.weight);
 }
 
 // The tiles of a segment, and each row's sum into xch[quarter][row].  A
@@ -375,19 +386,7 @@ __device__ __forceinline__ void soft_segment(const Soft &c, int it, int tiles, i
     for (int k = 0; k < 32; ++k) v[k] = k < 8 * kN ? lp[k < 8 * kN ? k : 0] : 0.f;
     const float sum = transpose_sum(v, c.lane);
     if (c.lane < 8 * kN)
-        stsf(c.sbase + kOffXch + 512 * (c.t >> 5) + 4 * (8 * (c.wg + 4 * (c.lane >> 3)) + (c.lane & 7)), sum);
-}
-
-// A warpgroup without rows keeps the hand-offs going.
-__device__ __forceinline__ void soft_idle(const Soft &c, int it, int tiles, bool &ok) {
-#pragma unroll 1
-    for (int j = 0; j < tiles; ++j, ++it) {
-        lazy_or_fail(ok, c.bx + 8 * (2 + (it & 1)), (it >> 1) & 1);
-        if (c.lane == 0) {
-            mbar_arrive(c.bx + 8 * (4 + (it & 1)));
-            mbar_arrive(c.bx + 8 * (8 + (it & 1)));
-        }
-    }
+        stsf(c.sbase + kOffXch + 512 * (c.t >> 5) + 4 * (32 * c.wg + c.lane), sum);
 }
 
 template <int kTerms>
@@ -413,12 +412,11 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
     const uint32_t bx = bar0 + 8 * 2 * kRaw;
     auto k_full = [&](int b) { return bx + 8 * b; };            // K levels -> MMA
     auto s_full = [&](int b) { return bx + 8 * (2 + b); };      // S ready (K levels read)
-    auto s_empty = [&](int b) { return bx + 8 * (4 + b); };     // S and the scales read
     auto v_full = [&](int b) { return bx + 8 * (6 + b); };      // V levels -> MMA
-    auto p_full = [&](int b) { return bx + 8 * (8 + b); };      // P' -> MMA
-    auto pv_done = [&](int b) { return bx + 8 * (10 + b); };    // V levels and P' read
-    auto sig_full = [&](int b) { return bx + 8 * (12 + b); };   // scales -> MMA
-    const uint32_t drained = bx + 8 * 14;
+    auto p_full = [&](int b) { return bx + 8 * (4 + b); };      // P' -> MMA; S and the scales read
+    auto pv_done = [&](int b) { return bx + 8 * (8 + b); };     // V levels and P' read
+    auto sig_full = [&](int b) { return bx + 8 * (10 + b); };   // scales -> MMA
+    const uint32_t drained = bx + 8 * 12;
     uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(smem + kOffTmem);
     float *sig_k = reinterpret_cast<float *>(smem + kOffSig);       // [4][128]
     float *sig_v = sig_k + kSig * kTileT;                           // [4][128]
@@ -437,9 +435,8 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
         for (int b = 0; b < 2; ++b) {
             mbar_init(k_full(b), 4);
             mbar_init(s_full(b), 1);
-            mbar_init(s_empty(b), kSoftWarps);
             mbar_init(v_full(b), 4);
-            mbar_init(p_full(b), kSoftWarps);
+            mbar_init(p_full(b), kPArrivals);
             mbar_init(pv_done(b), 1);
             mbar_init(sig_full(b), 1);
         }
@@ -458,7 +455,6 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
 
     bool ok = true;                                     // this warp's waits have all come through
     auto wait = [&](uint32_t bar, uint32_t parity) { wait_or_fail(ok, bar, parity); };
-    auto lazy = [&](uint32_t bar, uint32_t parity) { lazy_or_fail(ok, bar, parity); };
     // everyone but the producer and the idle warp, at the start of a segment
     // (twice) and at its end
     auto all_sync = [&]() { named_sync(1, 26 * 32); };
@@ -475,7 +471,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
                 for (int j = 0; j < s.tiles; ++j, ++it) {
                     const int st = it % kRaw;
                     if (it >= kRaw) {
-                        lazy(raw_empty(st), ((it / kRaw) - 1) & 1);
+                        wait(raw_empty(st), ((it / kRaw) - 1) & 1);
                         if (!ok) break;
                     }
                     const int t = (s.tile0 + j) * kTileT;
@@ -524,9 +520,10 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
                     bool moved = false;
                     if (jq < s.tiles && jq <= jp + 1) {
                         const int it = it0 + jq, b = it & 1;
+                        // (S and the scales of tile it - 2 are read: its P' is there,
+                        // or its PV would not have been issued)
                         if (__all_sync(kFull, mbar_test(k_full(b), (it >> 1) & 1) &&
-                                       mbar_test(sig_full(b), (it >> 1) & 1) &&
-                                       (it < 2 || mbar_test(s_empty(b), ((it >> 1) - 1) & 1)))) {
+                                       mbar_test(sig_full(b), (it >> 1) & 1))) {
                             tc::fence_after_sync();
                             if (leader) {
                                 const uint32_t d = tmem + kColS + 128 * b, ka = tmem + kColK + 64 * b;
@@ -673,8 +670,10 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
                 const int st = it % kRaw;
                 const uint32_t before = ((it >> 1) - 1) & 1;
                 wait(raw_full(st), (it / kRaw) & 1);
-                const uint32_t row = sbase + kOffRawK + st * kRawStride + t * kBlockBytes + 2;
-                const uint32_t a0 = row & ~3u, sh = (row & 3u) * 8u;
+                // the row's nibbles start 2 bytes behind a word boundary (even
+                // tokens) or 4 (odd ones): read from there, 32 lanes hit 32 banks
+                const uint32_t a0 = (sbase + kOffRawK + st * kRawStride + t * kBlockBytes) & ~3u;
+                const uint32_t sh = (t & 1) ? 32u : 16u;
                 if (it >= 2) wait(s_full(half), before);            // QK(it - 2) has read this buffer
                 tc::fence_after_sync();
                 uint32_t w[5];
@@ -688,7 +687,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         uint32_t l[4];
-                        word_levels(__funnelshift_r(w[i], w[i + 1], sh), l);
+                        word_levels(__funnelshift_rc(w[i], w[i + 1], sh), l);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) o[4 * i + e] = l[e];
                     }
@@ -714,7 +713,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         uint32_t l[4];
-                        word_levels(__funnelshift_r(w[i], w[i + 1], sh), l);
+                        word_levels(__funnelshift_rc(w[i], w[i + 1], sh), l);
                         dmq::sts128(to ^ (i << 4), l[0], l[1], l[2], l[3]);
                     }
                     w[0] = w[4];
@@ -821,20 +820,13 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
             all_sync();
             if (ws == 0 && lane == 0) *qmax = 0u;       // for the next segment (read before the barrier)
 
-            const Soft sc = {sbase, tmem, bx, t, lane, wg, c2};
+            const Soft sc = {sbase, tmem, bx, t, lane, wg, kPArrivals / 4 / ((nch + 3) >> 2), c2};
             const int t0 = s.tile0 * kTileT;
-            switch ((nch - wg + 3) >> 2) {              // chunks of this warpgroup
-                case 0: soft_idle(sc, it, s.tiles, ok); break;
-                case 1: soft_segment<kTerms, 1>(sc, it, s.tiles, t0, s.ctx, s.n, ok); break;
-                case 2: soft_segment<kTerms, 2>(sc, it, s.tiles, t0, s.ctx, s.n, ok); break;
-                default:
-                    if constexpr (kTerms == 1) {
-                        if (nch - wg <= 12)
-                            soft_segment<kTerms, 3>(sc, it, s.tiles, t0, s.ctx, s.n, ok);
-                        else
-                            soft_segment<kTerms, 4>(sc, it, s.tiles, t0, s.ctx, s.n, ok);
-                    }
-            }
+            const int mine = min(4, nch - 4 * wg);      // chunks of this warpgroup
+            if (mine == 4)
+                soft_segment<kTerms, 4>(sc, it, s.tiles, t0, s.ctx, s.n, ok);
+            else if (mine == 2)
+                soft_segment<kTerms, 2>(sc, it, s.tiles, t0, s.ctx, s.n, ok);
             it += s.tiles;
 
             // ---- the block's rows: thread = position of a dimension ----------
@@ -845,7 +837,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
             // sum_t P'_t (2n - 15) 2^-11 -> sum_t p S_v (2n - 15) / 15
             const float back = (ps > 0.f ? pow2_inv(ps) : 1.0f) * (2048.0f / 15.0f);
             named_sync(wg_bar, 128);
-            const int row = 8 * (wg + 4 * (t >> 3)) + (t & 7);
+            const int row = 32 * wg + t;
             if (t < 32 && row < s.rows) {
                 const float L = (xch[row] + xch[128 + row]) + (xch[256 + row] + xch[384 + row]);
                 if (whole)
@@ -856,7 +848,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
             const int d = dim_at(t);
             float *po = p.part_o + (int64_t)part_slot(s, cta) * p.rows * kD;
 #pragma unroll 1
-            for (int c = wg; c < nch; c += 4) {          // (V is done with its buffers)
+            for (int c = 4 * wg; c < min(nch, 4 * wg + 4); ++c) {   // (V is done with its buffers)
                 uint32_t o[8];
                 tc::tmem_ld8(t_lane + kColO + 8 * c, o);
                 tc::tmem_wait_ld();
