@@ -676,14 +676,19 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
                 const uint32_t sh = (t & 1) ? 32u : 16u;
                 if (it >= 2) wait(s_full(half), before);            // QK(it - 2) has read this buffer
                 tc::fence_after_sync();
+                // four words at a time: 32 levels, 16 columns; the next four are on
+                // their way meanwhile (reads past the row stay inside the stage)
+                const uint32_t v0 = a0 + kOffRawV - kOffRawK;
                 uint32_t w[5];
 #pragma unroll
                 for (int i = 0; i < 5; ++i) w[i] = dmq::lds32(a0 + 4 * i);
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c) {           // four words: 32 levels, 16 columns
-                    uint32_t o[16], nx[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) nx[i] = dmq::lds32(a0 + 4 * min(4 * c + 5 + i, 16));
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t o[16], nx[5];
+#pragma unroll
+                    for (int i = 1; i < 5; ++i)
+                        nx[i] = dmq::lds32(c < 3 ? a0 + 16 * (c + 1) + 4 * i : v0 + 4 * i);
+                    nx[0] = c < 3 ? w[4] : dmq::lds32(v0);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         uint32_t l[4];
@@ -692,29 +697,27 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
                         for (int e = 0; e < 4; ++e) o[4 * i + e] = l[e];
                     }
                     tc::tmem_st16(k_col + 16 * c, o);
-                    w[0] = w[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) w[i + 1] = nx[i];
+                    for (int i = 0; i < 5; ++i) w[i] = nx[i];
                 }
-                const uint32_t v0 = a0 + kOffRawV - kOffRawK;
-#pragma unroll
-                for (int i = 0; i < 5; ++i) w[i] = dmq::lds32(v0 + 4 * i);
                 tc::tmem_wait_st();
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(k_full(half));
                 if (it >= 2) wait(pv_done(half), before);
-#pragma unroll 1
-                for (int c = 0; c < 16; c += 4) {       // a word: eight levels, 16 bytes
-                    uint32_t nx[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) nx[i] = dmq::lds32(v0 + 4 * min(c + 5 + i, 16));
-                    const uint32_t to = (v_row ^ ((c & 4) << 4)) + (c >> 3) * 16384;
+                for (int c = 0; c < 16; c += 4) {       // a word: eight levels, 16 bytes
+                    uint32_t nx[4] = {};
+                    if (c < 12) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) nx[i] = dmq::lds32(v0 + 4 * (c + 5 + i));
+                    }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         uint32_t l[4];
                         word_levels(__funnelshift_rc(w[i], w[i + 1], sh), l);
-                        dmq::sts128(to ^ (i << 4), l[0], l[1], l[2], l[3]);
+                        dmq::sts128((v_row ^ (((c + i) & 7) << 4)) + ((c + i) >> 3) * 16384, l[0], l[1],
+                                    l[2], l[3]);
                     }
                     w[0] = w[4];
 #pragma unroll
