@@ -67,7 +67,7 @@ constexpr float kLowest = -1e30f;                       // running maximum befor
 // registers per thread by warpgroup: control, levels (2), softmax (4)
 // (setmaxnreg draws on what the block was launched with: the host refuses to
 // launch a build that compiled to fewer than kLaunchRegs)
-constexpr uint32_t kRegCtl = 56, kRegLev = 48, kRegSoft = 88;
+constexpr uint32_t kRegCtl = 40, kRegLev = 40, kRegSoft = 96;
 constexpr int kLaunchRegs = 72;
 static_assert(4 * kRegCtl + 8 * kRegLev + 16 * kRegSoft <= 28 * kLaunchRegs, "register split");
 
@@ -195,7 +195,7 @@ __device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t count) {
 // for up to kPollNs, or returns when the phase completes.
 constexpr uint32_t kPolls = 1u << 20, kPollNs = 2000;
 __device__ __forceinline__ void wait_or_fail(bool &ok, uint32_t bar, uint32_t parity) {
-    if (!ok) return;
+    if (!ok || __all_sync(kFull, mbar_test(bar, parity))) return;
     uint32_t left;
     asm volatile(
         "{\n .reg .pred p;\n mov.u32 %0, %3;\n"
@@ -682,13 +682,13 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
                 uint32_t w[5];
 #pragma unroll
                 for (int i = 0; i < 5; ++i) w[i] = dmq::lds32(a0 + 4 * i);
-#pragma unroll
+                uint32_t ka = a0;
+#pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
-                    uint32_t o[16], nx[5];
+                    uint32_t o[16], nx[4];
 #pragma unroll
-                    for (int i = 1; i < 5; ++i)
-                        nx[i] = dmq::lds32(c < 3 ? a0 + 16 * (c + 1) + 4 * i : v0 + 4 * i);
-                    nx[0] = c < 3 ? w[4] : dmq::lds32(v0);
+                    for (int i = 0; i < 4; ++i) nx[i] = dmq::lds32(ka + 20 + 4 * i);
+                    ka += 16;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         uint32_t l[4];
@@ -697,27 +697,29 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
                         for (int e = 0; e < 4; ++e) o[4 * i + e] = l[e];
                     }
                     tc::tmem_st16(k_col + 16 * c, o);
+                    w[0] = w[4];
 #pragma unroll
-                    for (int i = 0; i < 5; ++i) w[i] = nx[i];
+                    for (int i = 0; i < 4; ++i) w[i + 1] = nx[i];
                 }
+#pragma unroll
+                for (int i = 0; i < 5; ++i) w[i] = dmq::lds32(v0 + 4 * i);
                 tc::tmem_wait_st();
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(k_full(half));
                 if (it >= 2) wait(pv_done(half), before);
+                uint32_t va = v0;
+#pragma unroll 1
+                for (int c = 0; c < 16; c += 4, va += 16) {       // a word: eight levels, 16 bytes
+                    uint32_t nx[4];
 #pragma unroll
-                for (int c = 0; c < 16; c += 4) {       // a word: eight levels, 16 bytes
-                    uint32_t nx[4] = {};
-                    if (c < 12) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) nx[i] = dmq::lds32(v0 + 4 * (c + 5 + i));
-                    }
+                    for (int i = 0; i < 4; ++i) nx[i] = dmq::lds32(va + 20 + 4 * i);
+                    const uint32_t to = (v_row ^ ((c & 4) << 4)) + (c >> 3) * 16384;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         uint32_t l[4];
                         word_levels(__funnelshift_rc(w[i], w[i + 1], sh), l);
-                        dmq::sts128((v_row ^ (((c + i) & 7) << 4)) + ((c + i) >> 3) * 16384, l[0], l[1],
-                                    l[2], l[3]);
+                        dmq::sts128(to ^ (i << 4), l[0], l[1], l[2], l[3]);
                     }
                     w[0] = w[4];
 #pragma unroll
