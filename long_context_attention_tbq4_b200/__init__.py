@@ -10,7 +10,6 @@ indices) in a Hadamard-rotated domain, and attention dequantises the raw
 blocks inside its inner loop (trefon.com, "Kontekst 262K na jednej RTX 4090:
 co dodalem do llama.cpp-turboq", section "Od czego zaczalem").
 """
-import contextlib
 import ctypes as C
 
 import numpy as np
@@ -337,85 +336,113 @@ def tbq4_attn_prefill_chunk(q, n_cached, k_cache, v_cache, softmax_scale, sign_s
 _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}    # tbq4_dtype
 
 
-def _one_device(first, *rest):
-    """The device that every given tensor (None: not given) lies on."""
-    for t in rest:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors on {first.device} and {t.device}: one device is needed")
-    return first.device
+# The calls below serve single decode steps, so the host's share counts: a
+# check reads each attribute once, and devices are compared by index.
+
+def _check(name, t, dtype, ndim, index):
+    """A contiguous CUDA tensor of this type and rank on device `index`."""
+    if not (t.dtype is dtype and t.dim() == ndim and t.is_contiguous() and t.get_device() == index):
+        _need(t, dtype, name, ndim)
+        raise ValueError(f"{name} lies on {t.device}, other tensors on cuda:{index}")
 
 
-def _on(device):
-    """Makes `device` current for a call whose tensors lie on another one."""
-    if device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+def _device_index(t, name):
+    """The index of the device that t, and with it all of a call, lies on."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return t.get_device()
 
 
-def _stream_on(stream, device):
+def _stream_on(stream, index):
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
-        raise ValueError(f"stream on {stream.device}, tensors on {device}")
+        return torch.cuda.current_stream(index).cuda_stream
+    if stream.device.index != index:
+        raise ValueError(f"stream on {stream.device}, tensors on cuda:{index}")
     return stream.cuda_stream
 
 
-def _ptr_or_null(t):
-    return t.data_ptr() if t is not None else None
+def _call(name, index, *args):
+    """The library's function `name`, with device `index` current."""
+    if index == torch.cuda.current_device():
+        code = getattr(lib, name)(*args)
+    else:
+        with torch.cuda.device(index):
+            code = getattr(lib, name)(*args)
+    if code:
+        raise Tbq4Error(code, name)
 
 
-def _need_rows(t, name, dtype=None, heads=None, tokens=None):
-    """Rows of 128 at any token and head stride; returns those strides."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype not in _DTYPES or (dtype is not None and t.dtype != dtype):
-        raise TypeError(f"{name} must be {dtype or 'float32, float16 or bfloat16'}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[2] != D or t.stride(2) != 1:
-        raise ValueError(f"{name} must be [tokens][heads][128] with adjacent channels, "
-                         f"got {tuple(t.shape)} with strides {t.stride()}")
-    if (heads is not None and t.shape[1] != heads) or (tokens is not None and t.shape[0] != tokens):
-        raise ValueError(f"{name} must be [{tokens}][{heads}][128], got {tuple(t.shape)}")
+def _rows(name, t, dtype, index, tokens, heads):
+    """Rows of 128 at any token and head stride: pointer and strides."""
+    shape, (tok, head, one) = t.shape, t.stride()
+    if not (t.dtype is dtype and t.get_device() == index and shape[2] == D and one == 1
+            and shape[0] == tokens and shape[1] == heads):
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.get_device() != index:
+            raise ValueError(f"{name} lies on {t.device}, other tensors on cuda:{index}")
+        raise ValueError(f"{name} must be [{tokens}][{heads}][128] with adjacent channels, "
+                         f"got {tuple(shape)} with strides {t.stride()}")
     # the stride of a dimension of one is never used
-    return (t.stride(0) if t.shape[0] > 1 else 0), (t.stride(1) if t.shape[1] > 1 else 0)
+    return t.data_ptr(), tok if tokens > 1 else 0, head if heads > 1 else 0
 
 
-def _rope_append(name, k, v, slots, inv_freq, kc, vc, Hkv, B, layout, table, q, positions, seq_ids,
+def _rope_append(name, k, v, slots, inv_freq, kc, vc, Hkv, B, layout, index, q, positions, seq_ids,
                  interleaved, sign_seed, q_out, stream):
-    k_tok, k_head = _need_rows(k, "k", heads=Hkv)
-    n = k.shape[0]
-    v_tok, v_head = _need_rows(v, "v", k.dtype, Hkv, n)
-    _need(slots, torch.int32, "slots", 1)
-    rot = 0
-    if inv_freq is not None:
-        _need(inv_freq, torch.float64, "inv_freq", 1)
-        rot = 2 * inv_freq.shape[0]
-    for t, what in ((positions, "positions"), (seq_ids, "seq_ids")):
-        if t is not None:
-            _need(t, torch.int32, what, 1)
-            if t.shape[0] != n:
-                raise ValueError(f"{what} must be [{n}], got {tuple(t.shape)}")
-    if slots.shape[0] != n:
-        raise ValueError(f"slots must be [{n}], got {tuple(slots.shape)}")
-    Hq = q_tok = q_head = 0
+    for t, what in ((k, "k"), (v, "v"), (q, "q")):
+        if t is not None and (not isinstance(t, torch.Tensor) or t.dtype not in _DTYPES or t.dim() != 3):
+            raise TypeError(f"{what} must be a [tokens][heads][128] CUDA tensor of float32, float16 or "
+                            f"bfloat16")
+    dtype, n = k.dtype, k.shape[0]
+    krows = _rows("k", k, dtype, index, n, Hkv)
+    vrows = _rows("v", v, dtype, index, n, Hkv)
+    Hq, qrows, out_ptr = 0, (None, 0, 0), None
     if q is not None:
-        q_tok, q_head = _need_rows(q, "q", k.dtype, tokens=n)
         Hq = q.shape[1]
+        qrows = _rows("q", q, dtype, index, n, Hq)
         if q_out is None:
-            q_out = torch.empty((n, Hq, D), dtype=q.dtype, device=q.device)
-        _need(q_out, q.dtype, "q_out", 3)
-        if q_out.shape != q.shape:
-            raise ValueError(f"q_out must be {tuple(q.shape)}, got {tuple(q_out.shape)}")
+            q_out = torch.empty((n, Hq, D), dtype=dtype, device=q.device)
+        else:
+            _check("q_out", q_out, dtype, 3, index)
+            if q_out.shape != q.shape:
+                raise ValueError(f"q_out must be {tuple(q.shape)}, got {tuple(q_out.shape)}")
+        out_ptr = q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
-    device = _one_device(k, v, slots, inv_freq, kc, vc, table, q, positions, seq_ids, q_out)
-    with _on(device):
-        check(getattr(lib, name)(
-            _ptr_or_null(q), q_tok, q_head, k.data_ptr(), k_tok, k_head, v.data_ptr(), v_tok, v_head,
-            _DTYPES[k.dtype], n, B, Hq, Hkv, _ptr_or_null(seq_ids), slots.data_ptr(),
-            _ptr_or_null(positions), _ptr_or_null(inv_freq), rot, int(bool(interleaved)), *layout,
-            sign_seed, kc.data_ptr(), vc.data_ptr(), _ptr_or_null(q_out),
-            _stream_on(stream, device)), name)
+    ids = pos = freq = None
+    rot = 0
+    _check("slots", slots, torch.int32, 1, index)
+    wrong = slots.shape[0] != n
+    if positions is not None:
+        _check("positions", positions, torch.int32, 1, index)
+        wrong |= positions.shape[0] != n
+        pos = positions.data_ptr()
+    if seq_ids is not None:
+        _check("seq_ids", seq_ids, torch.int32, 1, index)
+        wrong |= seq_ids.shape[0] != n
+        ids = seq_ids.data_ptr()
+    if wrong:
+        raise ValueError(f"slots, positions and seq_ids must be [{n}]")
+    if inv_freq is not None:
+        _check("inv_freq", inv_freq, torch.float64, 1, index)
+        rot = 2 * inv_freq.shape[0]
+        freq = inv_freq.data_ptr()
+    _call(name, index, *qrows, *krows, *vrows, _DTYPES[dtype], n, B, Hq, Hkv, ids, slots.data_ptr(),
+          pos, freq, rot, 1 if interleaved else 0, *layout, sign_seed, kc.data_ptr(), vc.data_ptr(),
+          out_ptr, _stream_on(stream, index))
     return q_out
+
+
+def _cache_pair(k_cache, v_cache, names, block=BLOCK_BYTES):
+    """Device index and [.., .., .., 66] shape of a K and a V cache or pool."""
+    index = _device_index(k_cache, names[0])
+    _check(names[0], k_cache, torch.uint8, 4, index)
+    _check(names[1], v_cache, torch.uint8, 4, index)
+    shape = k_cache.shape
+    if shape[3] != block or v_cache.shape != shape:
+        raise ValueError(f"{names[0]} and {names[1]} must have one shape that ends in {block}, got "
+                         f"{tuple(shape)} and {tuple(v_cache.shape)}")
+    return index, shape
 
 
 def tbq4_rope_append(k, v, slots, inv_freq, k_cache, v_cache, q=None, positions=None, seq_ids=None,
@@ -428,13 +455,9 @@ def tbq4_rope_append(k, v, slots, inv_freq, k_cache, v_cache, q=None, positions=
     [rot_dim / 2] (None: no rotation); caches uint8 [B][Hkv][capacity][66]
     (written).  Returns the rotated queries, [n][Hq][128] in q's dtype (None
     without q)."""
-    _need(k_cache, torch.uint8, "k_cache", 4)
-    _need(v_cache, torch.uint8, "v_cache", 4)
-    B, Hkv, cap, nb = k_cache.shape
-    if nb != BLOCK_BYTES or v_cache.shape != k_cache.shape:
-        raise ValueError("k_cache and v_cache must be [B][Hkv][capacity][66]")
+    index, (B, Hkv, cap, _) = _cache_pair(k_cache, v_cache, ("k_cache", "v_cache"))
     return _rope_append("tbq4_rope_append", k, v, slots, inv_freq, k_cache, v_cache, Hkv, B, (cap,),
-                        None, q, positions, seq_ids, interleaved, sign_seed, q_out, stream)
+                        index, q, positions, seq_ids, interleaved, sign_seed, q_out, stream)
 
 
 def tbq4_rope_append_paged(k, v, slots, inv_freq, block_table, k_pool, v_pool, q=None,
@@ -442,15 +465,12 @@ def tbq4_rope_append_paged(k, v, slots, inv_freq, block_table, k_pool, v_pool, q
                            stream=None):
     """As tbq4_rope_append, into page pools uint8 [n_pages][Hkv][page_size][66]
     through block_table int32 [B][max_pages]."""
-    _need(block_table, torch.int32, "block_table", 2)
-    n_pages, Hkv, page_size = _pool_shape(k_pool, "k_pool")
-    _pool_shape(v_pool, "v_pool")
-    if v_pool.shape != k_pool.shape:
-        raise ValueError("k_pool and v_pool differ in shape")
-    return _rope_append("tbq4_rope_append_paged", k, v, slots, inv_freq, k_pool, v_pool, Hkv,
-                        block_table.shape[0],
-                        (block_table.data_ptr(), block_table.shape[1], page_size, n_pages),
-                        block_table, q, positions, seq_ids, interleaved, sign_seed, q_out, stream)
+    index, (n_pages, Hkv, page_size, _) = _cache_pair(k_pool, v_pool, ("k_pool", "v_pool"))
+    _check("block_table", block_table, torch.int32, 2, index)
+    B, max_pages = block_table.shape
+    return _rope_append("tbq4_rope_append_paged", k, v, slots, inv_freq, k_pool, v_pool, Hkv, B,
+                        (block_table.data_ptr(), max_pages, page_size, n_pages), index, q, positions,
+                        seq_ids, interleaved, sign_seed, q_out, stream)
 
 
 def tree_mask(parents):
@@ -478,46 +498,45 @@ def tbq4_tree_workspace_bytes(B, T, Hq, Hkv) -> int:
     return int(lib.tbq4_tree_workspace_bytes(B, T, Hq, Hkv))
 
 
-def _attn_tree(name, q, kc, vc, Hkv, layout, table, ctx_lens, mask, softmax_scale, sign_seed, n_nodes,
-               workspace, out, out_dtype, stream):
+def _attn_tree(name, q, kc, vc, Hkv, B, cap, paged, index, ctx_lens, mask, softmax_scale, sign_seed,
+               n_nodes, workspace, out, out_dtype, stream):
     if not isinstance(q, torch.Tensor) or q.dtype not in _DTYPES:
         raise TypeError("q must be a float32, float16 or bfloat16 CUDA tensor")
-    _need(q, q.dtype, "q", 4)
-    _need(ctx_lens, torch.int32, "ctx_lens", 1)
-    _need(mask, torch.int64, "tree_mask")
-    B, T, Hq, d = q.shape
-    if d != D or ctx_lens.shape[0] != B:
+    _check("q", q, q.dtype, 4, index)
+    Bq, T, Hq, d = shape = q.shape
+    _check("ctx_lens", ctx_lens, torch.int32, 1, index)
+    if d != D or Bq != B or ctx_lens.shape[0] != B:
         raise ValueError("shape mismatch between q, caches and ctx_lens")
-    if tuple(mask.shape) not in ((T,), (B, T)):
+    _check("tree_mask", mask, torch.int64, mask.dim(), index)
+    per = mask.numel() // T if T else 0
+    if mask.shape[-1:] != (T,) or (mask.dim() == 2 and per != B) or not 1 <= mask.dim() <= 2:
         raise ValueError(f"tree_mask must be [{T}] or [{B}][{T}], got {tuple(mask.shape)}")
+    nodes = None
     if n_nodes is not None:
-        _need(n_nodes, torch.int32, "n_nodes", 1)
+        _check("n_nodes", n_nodes, torch.int32, 1, index)
         if n_nodes.shape[0] != B:
             raise ValueError(f"n_nodes must be [{B}], got {tuple(n_nodes.shape)}")
+        nodes = n_nodes.data_ptr()
     if workspace is None:
-        workspace = torch.empty(max(tbq4_tree_workspace_bytes(B, T, Hq, Hkv), 1), dtype=torch.uint8,
-                                device=q.device)
-    elif not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
+        workspace = torch.empty(max(lib.tbq4_tree_workspace_bytes(B, T, Hq, Hkv), 1),
+                                dtype=torch.uint8, device=q.device)
+    elif not workspace.is_contiguous() or workspace.get_device() != index:
+        raise ValueError(f"workspace must be contiguous, on cuda:{index}")
     if out is None:
         if out_dtype is None:
-            out_dtype = torch.bfloat16 if q.dtype == torch.bfloat16 else torch.float16
-        out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
-    elif out_dtype is not None and out.dtype != out_dtype:
+            out_dtype = torch.bfloat16 if q.dtype is torch.bfloat16 else torch.float16
+        out = torch.empty(shape, dtype=out_dtype, device=q.device)
+    elif out_dtype is not None and out.dtype is not out_dtype:
         raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
     if out.dtype not in (torch.float16, torch.bfloat16):
         raise TypeError(f"out must be float16 or bfloat16, got {out.dtype}")
-    _need(out, out.dtype, "out", 4)
-    if out.shape != q.shape:
-        raise ValueError(f"out must be {tuple(q.shape)}, got {tuple(out.shape)}")
-    device = _one_device(q, kc, vc, table, ctx_lens, mask, n_nodes, workspace, out)
-    with _on(device):
-        check(getattr(lib, name)(
-            q.data_ptr(), _DTYPES[q.dtype], kc.data_ptr(), vc.data_ptr(), *(layout if table is not None else ()),
-            ctx_lens.data_ptr(), _ptr_or_null(n_nodes), mask.data_ptr(), T if mask.dim() == 2 else 0,
-            B, T, Hq, Hkv, *(layout if table is None else ()), float(softmax_scale), sign_seed,
-            workspace.data_ptr(), workspace.numel() * workspace.element_size(), out.data_ptr(),
-            _DTYPES[out.dtype], _stream_on(stream, device)), name)
+    _check("out", out, out.dtype, 4, index)
+    if out.shape != shape:
+        raise ValueError(f"out must be {tuple(shape)}, got {tuple(out.shape)}")
+    _call(name, index, q.data_ptr(), _DTYPES[q.dtype], kc.data_ptr(), vc.data_ptr(), *paged,
+          ctx_lens.data_ptr(), nodes, mask.data_ptr(), T if mask.dim() == 2 else 0, B, T, Hq, Hkv, *cap,
+          softmax_scale, sign_seed, workspace.data_ptr(), workspace.nbytes, out.data_ptr(),
+          _DTYPES[out.dtype], _stream_on(stream, index))
     return out
 
 
@@ -530,13 +549,9 @@ def tbq4_attn_tree(q, k_cache, v_cache, ctx_lens, tree_mask, softmax_scale, sign
     for all): bit j of entry i set where node i sees node j.  Returns
     [B][T][Hq][128] in out's dtype (default: bfloat16 for bfloat16 queries,
     else float16); rows of nodes >= n_nodes[b] are not written."""
-    _need(k_cache, torch.uint8, "k_cache", 4)
-    _need(v_cache, torch.uint8, "v_cache", 4)
-    B, Hkv, cap, nb = k_cache.shape
-    if nb != BLOCK_BYTES or v_cache.shape != k_cache.shape or B != q.shape[0]:
-        raise ValueError("shape mismatch between q and caches")
-    return _attn_tree("tbq4_attn_tree", q, k_cache, v_cache, Hkv, (cap,), None, ctx_lens, tree_mask,
-                      softmax_scale, sign_seed, n_nodes, workspace, out, out_dtype, stream)
+    index, (B, Hkv, cap, _) = _cache_pair(k_cache, v_cache, ("k_cache", "v_cache"))
+    return _attn_tree("tbq4_attn_tree", q, k_cache, v_cache, Hkv, B, (cap,), (), index, ctx_lens,
+                      tree_mask, softmax_scale, sign_seed, n_nodes, workspace, out, out_dtype, stream)
 
 
 def tbq4_attn_tree_paged(q, k_pool, v_pool, block_table, ctx_lens, tree_mask, softmax_scale,
@@ -544,41 +559,47 @@ def tbq4_attn_tree_paged(q, k_pool, v_pool, block_table, ctx_lens, tree_mask, so
                          stream=None):
     """As tbq4_attn_tree, over page pools uint8 [n_pages][Hkv][page_size][66]
     through block_table int32 [B][max_pages]."""
-    _need(block_table, torch.int32, "block_table", 2)
-    n_pages, Hkv, page_size = _pool_shape(k_pool, "k_pool")
-    _pool_shape(v_pool, "v_pool")
-    if v_pool.shape != k_pool.shape or block_table.shape[0] != q.shape[0]:
-        raise ValueError("shape mismatch between q, block_table and pools")
-    return _attn_tree("tbq4_attn_tree_paged", q, k_pool, v_pool, Hkv,
-                      (block_table.data_ptr(), block_table.shape[1], page_size, n_pages), block_table,
-                      ctx_lens, tree_mask, softmax_scale, sign_seed, n_nodes, workspace, out,
-                      out_dtype, stream)
+    index, (n_pages, Hkv, page_size, _) = _cache_pair(k_pool, v_pool, ("k_pool", "v_pool"))
+    _check("block_table", block_table, torch.int32, 2, index)
+    B, max_pages = block_table.shape
+    return _attn_tree("tbq4_attn_tree_paged", q, k_pool, v_pool, Hkv, B, (),
+                      (block_table.data_ptr(), max_pages, page_size, n_pages), index, ctx_lens,
+                      tree_mask, softmax_scale, sign_seed, n_nodes, workspace, out, out_dtype, stream)
 
 
-def _tree_accept(name, ks, vs, shape, B, Hkv, layout, table, ctx_lens, path, n_accept, new_lens, stream):
-    if len(ks) != len(vs) or not ks:
-        raise ValueError(f"{len(ks)} K and {len(vs)} V caches: as many of each, at least one")
+def _tree_accept(name, ks, vs, shape, B, cap, paged, index, ctx_lens, path, n_accept, new_lens, stream):
+    n = len(ks)
+    if n != len(vs):
+        raise ValueError(f"{n} K and {len(vs)} V caches: as many of each")
+    u8 = torch.uint8
     for c in (*ks, *vs):
-        _need(c, torch.uint8, "each cache", 4)
-        if c.shape != shape:
+        if not (c.dtype is u8 and c.shape == shape and c.is_contiguous() and c.get_device() == index):
+            _check("each cache", c, u8, 4, index)
             raise ValueError("the caches differ in shape")
-    _need(ctx_lens, torch.int32, "ctx_lens", 1)
-    _need(path, torch.int32, "path", 2)
-    _need(n_accept, torch.int32, "n_accept", 1)
+    for t, what, ndim in ((ctx_lens, "ctx_lens", 1), (path, "path", 2), (n_accept, "n_accept", 1)):
+        _check(what, t, torch.int32, ndim, index)
     if new_lens is None:
         new_lens = torch.empty_like(ctx_lens)
-    _need(new_lens, torch.int32, "new_lens", 1)
+    else:
+        _check("new_lens", new_lens, torch.int32, 1, index)
     if not B == ctx_lens.shape[0] == path.shape[0] == n_accept.shape[0] == new_lens.shape[0]:
         raise ValueError("shape mismatch between caches, ctx_lens, path, n_accept and new_lens")
-    device = _one_device(ctx_lens, path, n_accept, new_lens, table, *ks, *vs)
-    n = len(ks)
-    with _on(device):
-        check(getattr(lib, name)(
-            (C.c_void_p * n)(*[c.data_ptr() for c in ks]), (C.c_void_p * n)(*[c.data_ptr() for c in vs]),
-            n, *(layout if table is not None else ()), ctx_lens.data_ptr(), path.data_ptr(),
-            n_accept.data_ptr(), path.shape[1], B, Hkv, *(layout if table is None else ()),
-            new_lens.data_ptr(), _stream_on(stream, device)), name)
+    ptrs = C.c_void_p * n
+    _call(name, index, ptrs(*[c.data_ptr() for c in ks]), ptrs(*[c.data_ptr() for c in vs]), n, *paged,
+          ctx_lens.data_ptr(), path.data_ptr(), n_accept.data_ptr(), path.shape[1], B, shape[1], *cap,
+          new_lens.data_ptr(), _stream_on(stream, index))
     return new_lens
+
+
+def _first_cache(caches, name):
+    """Device index and shape of the first of a list of caches."""
+    if not caches:
+        raise ValueError("no caches")
+    index = _device_index(caches[0], name)
+    _check(name, caches[0], torch.uint8, 4, index)
+    if caches[0].shape[3] != BLOCK_BYTES:
+        raise ValueError(f"{name} must end in {BLOCK_BYTES}, got {tuple(caches[0].shape)}")
+    return index, caches[0].shape
 
 
 def tbq4_tree_accept(k_caches, v_caches, ctx_lens, path, n_accept, new_lens=None, stream=None):
@@ -586,24 +607,21 @@ def tbq4_tree_accept(k_caches, v_caches, ctx_lens, path, n_accept, new_lens=None
     [B][Hkv][capacity][66], written): block ctx_lens[b] + i becomes block
     ctx_lens[b] + path[b][i] for i < n_accept[b].  path int32 [B][max_path],
     ctx_lens and n_accept int32 [B].  Returns the new lengths, int32 [B]."""
-    _need(k_caches[0], torch.uint8, "each cache", 4)
-    shape = k_caches[0].shape
-    if shape[3] != BLOCK_BYTES:
-        raise ValueError("caches must be [B][Hkv][capacity][66]")
-    return _tree_accept("tbq4_tree_accept", k_caches, v_caches, shape, shape[0], shape[1], (shape[2],),
-                        None, ctx_lens, path, n_accept, new_lens, stream)
+    index, shape = _first_cache(k_caches, "each cache")
+    return _tree_accept("tbq4_tree_accept", k_caches, v_caches, shape, shape[0], (shape[2],), (), index,
+                        ctx_lens, path, n_accept, new_lens, stream)
 
 
 def tbq4_tree_accept_paged(k_pools, v_pools, block_table, ctx_lens, path, n_accept, new_lens=None,
                            stream=None):
     """As tbq4_tree_accept, over page pools (lists of uint8
     [n_pages][Hkv][page_size][66]) that share block_table int32 [B][max_pages]."""
-    _need(block_table, torch.int32, "block_table", 2)
-    n_pages, Hkv, page_size = _pool_shape(k_pools[0], "each pool")
-    return _tree_accept("tbq4_tree_accept_paged", k_pools, v_pools, k_pools[0].shape,
-                        block_table.shape[0], Hkv,
-                        (block_table.data_ptr(), block_table.shape[1], page_size, n_pages), block_table,
-                        ctx_lens, path, n_accept, new_lens, stream)
+    index, shape = _first_cache(k_pools, "each pool")
+    _check("block_table", block_table, torch.int32, 2, index)
+    B, max_pages = block_table.shape
+    return _tree_accept("tbq4_tree_accept_paged", k_pools, v_pools, shape, B, (),
+                        (block_table.data_ptr(), max_pages, shape[2], shape[0]), index, ctx_lens, path,
+                        n_accept, new_lens, stream)
 
 
 def tbq4_set_timing_events(before=None, after=None):
