@@ -675,6 +675,9 @@ tbq4_status tbq4_attn_prefill_chunk(const uint16_t *q, int n_new, int64_t n_cach
 
 namespace {
 
+// Warps per SM that rope-append spreads few tokens over.
+constexpr int kRopeFill = 32;
+
 size_t elem_bytes(int dtype) { return dtype == TBQ4_F32 ? 4 : 2; }
 bool elem_type(int dtype) {
     return dtype == TBQ4_F32 || dtype == TBQ4_F16 || dtype == TBQ4_BF16;
@@ -689,6 +692,14 @@ struct Rows {
         return aligned(p, 16) && tok >= 0 && head >= 0 && tok % per == 0 && head % per == 0;
     }
 };
+
+template <int kType>
+const void *rope_kernel(int rot_dim, int interleaved) {
+    if (rot_dim == 0) return (const void *)rope_append_kernel<kType, kRopeNone>;
+    if (interleaved) return (const void *)rope_append_kernel<kType, kRopeInterleaved>;
+    if (rot_dim == kD) return (const void *)rope_append_kernel<kType, kRopeAll>;
+    return (const void *)rope_append_kernel<kType, kRopePart>;
+}
 
 tbq4_status rope_impl(const Rows &q, const Rows &k, const Rows &v, int dtype, int n_tokens, int B,
                       int Hq, int Hkv, const int32_t *seq_ids, const int32_t *slots,
@@ -749,8 +760,20 @@ tbq4_status rope_impl(const Rows &q, const Rows &k, const Rows &v, int dtype, in
     p.vc = vc;
     p.q_out = q_out;
     p.q_out_elems = (int64_t)n_tokens * Hq * kD;
-    const int blocks = std::min(n_tokens, kNumSMs * 64);
-    rope_append_kernel<<<blocks, kRopeWarps * 32, 0, (cudaStream_t)stream>>>(p);
+    // a warp per token; with few tokens several warps share one, down to a pair
+    // of rows each (one token of 24/4 heads: 6.5 us, 7.6 with its rows over the
+    // eight warps of one block)
+    const int pairs = (Hq + 1) / 2 + 2 * ((Hkv + 1) / 2);
+    const int parts = (int)std::max<int64_t>(
+        1, std::min<int64_t>(pairs, (int64_t)kNumSMs * kRopeFill / n_tokens));
+    const int64_t blocks = ceil_div((int64_t)n_tokens * parts, kRopeWarps);
+    const void *fn = dtype == TBQ4_F32   ? rope_kernel<kElemF32>(rot_dim, interleaved)
+                     : dtype == TBQ4_F16 ? rope_kernel<kElemF16>(rot_dim, interleaved)
+                                         : rope_kernel<kElemBF16>(rot_dim, interleaved);
+    void *args[] = {&p, const_cast<int *>(&parts)};
+    if (cudaLaunchKernel(fn, dim3((unsigned)blocks), dim3(kRopeWarps * 32), args, 0,
+                         (cudaStream_t)stream) != cudaSuccess)
+        return TBQ4_ERR_LAUNCH;
     return launch_status();
 }
 
@@ -878,7 +901,7 @@ tbq4_status accept_impl(uint8_t *const *k_caches, uint8_t *const *v_caches, int 
     if (n_layers <= 0 || n_layers > kMaxAcceptLayers || B <= 0 || Hkv <= 0 || max_path <= 0 ||
         max_path > kMaxPath || new_lens == ctx_lens)
         return TBQ4_ERR_SHAPE;
-    if (capacity <= 0 || capacity % 8 != 0) return TBQ4_ERR_CAPACITY;
+    if (capacity <= 0 || capacity % 8 != 0 || capacity > INT32_MAX) return TBQ4_ERR_CAPACITY;
     const int per = std::min(n_layers, kAcceptLayers);
     if ((int64_t)2 * per * B * Hkv > (int64_t)kAcceptWarps * INT32_MAX) return TBQ4_ERR_SHAPE;
     const uint8_t *all[2 * kMaxAcceptLayers];
@@ -917,8 +940,8 @@ tbq4_status accept_impl(uint8_t *const *k_caches, uint8_t *const *v_caches, int 
         p.n_caches = 2 * n;
         p.new_lens = l0 == 0 ? new_lens : nullptr;
         const int64_t items = (int64_t)p.n_caches * B * Hkv;
-        tree_accept_kernel<<<(unsigned)ceil_div(items, kAcceptWarps), kAcceptWarps * 32, 0,
-                             (cudaStream_t)stream>>>(p);
+        tree_accept_kernel<<<(unsigned)ceil_div(items, kAcceptWarps), kAcceptWarps * 32,
+                             kAcceptWarps * accept_warp_bytes(max_path), (cudaStream_t)stream>>>(p);
     }
     return launch_status();
 }

@@ -52,8 +52,10 @@ def test_refusals(paged):
     if paged:
         assert r(table=None) == 1
         assert r(page=40) == 3
+        assert r(max_pages=1 << 27) == 4               # more slots than 32 bits number
     else:
         assert r(cap=60) == 4
+        assert r(cap=1 << 31) == 4
 
 
 @pytest.mark.gpu
