@@ -252,9 +252,8 @@ __device__ __forceinline__ void soft_tile(const Soft &c, int it, bool first, int
     float top = -INFINITY;
 #pragma unroll
     for (int i0 = 0; i0 < kN; i0 += 2) {
-        uint32_t r[2][8];
-        tc::tmem_ld8(s_col + 8 * i0, r[0]);
-        tc::tmem_ld8(s_col + 8 * i0 + 8, r[1]);
+        float r[16];
+        tc::tmem_ld16(s_col + 8 * i0, r);
         tc::tmem_wait_ld();
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -265,8 +264,8 @@ __device__ __forceinline__ void soft_tile(const Soft &c, int it, bool first, int
             float x[8];                                            // log2 p: S skc - m, hidden ones -inf
 #pragma unroll
             for (int k = 0; k < 8; k += 2) {
-                unpack2(fma2(pack2(__uint_as_float(r[e][k]), __uint_as_float(r[e][k + 1])),
-                             pack2(skc, skc), pack2(nm[k], nm[k + 1])), x[k], x[k + 1]);
+                unpack2(fma2(pack2(r[8 * e + k], r[8 * e + k + 1]), pack2(skc, skc),
+                             pack2(nm[k], nm[k + 1])), x[k], x[k + 1]);
                 if (!sees(i, k)) x[k] = -INFINITY;
                 if (!sees(i, k + 1)) x[k + 1] = -INFINITY;
             }
@@ -489,63 +488,46 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
                 const uint64_t q_desc = tc::desc_sw128(sbase + kOffQ);
                 const uint64_t v_desc = tc::desc_mn_sw128(sbase + kOffV, 16384);
                 const uint64_t p_desc = tc::desc_mn_sw128(sbase + kOffP, 16384);
-                int jq = 0, jp = 0;                     // next QK and PV of this segment
-                uint32_t idle = 0;
-                while (ok && jp < s.tiles) {
-                    bool moved = false;
-                    if (jq < s.tiles && jq <= jp + 1) {
-                        const int it = it0 + jq, b = it & 1;
-                        // (S and the scales of tile it - 2 are read: its P' is there,
-                        // or its PV would not have been issued)
-                        if (__all_sync(kFull, mbar_test(k_full(b), (it >> 1) & 1) &&
-                                       mbar_test(sig_full(b), (it >> 1) & 1))) {
-                            tc::fence_after_sync();
-                            if (leader) {
-                                const uint32_t d = tmem + kColS + 128 * b, ka = tmem + kColK + 64 * b;
-                                tc::mma_ts_c<false>(d, ka, q_desc, idesc_qk);
+                // QK two tiles ahead: S of tile j - 2 and its scales are read once
+                // its P' is there
+#pragma unroll 1
+                for (int j = 0; j < s.tiles + 2; ++j) {
+                    const int it = it0 + j, b = it & 1;
+                    const uint32_t par = (it >> 1) & 1;
+                    if (j >= 2) {
+                        wait(v_full(b), par ^ 1);
+                        wait(p_full(b), par ^ 1);
+                        tc::fence_after_sync();
+                        if (leader) {
+                            const uint64_t va = v_desc + 2048 * b, pb = p_desc + 2048 * b;
+                            if (j > 2)
+                                tc::mma_ss_c<true>(tmem + kColO, va, pb, idesc_pv);
+                            else
+                                tc::mma_ss_c<false>(tmem + kColO, va, pb, idesc_pv);
 #pragma unroll
-                                for (int i = 1; i < 8 * kTerms; ++i)     // descriptors count 16 bytes
-                                    tc::mma_ts_c<true>(d, ka + 8 * (i & 7),
-                                                       q_desc + (i >> 3) * (kRows * 16) +
-                                                           ((i & 7) >> 2) * (kRows * 8) + (i & 3) * 2,
-                                                       idesc_qk);
-                                tc::mma_commit(s_full(b));
-                            }
-                            __syncwarp();
-                            ++jq;
-                            moved = true;
+                            for (int i = 1; i < 8 * kTerms; ++i)         // descriptors count 16 bytes
+                                tc::mma_ss_c<true>(tmem + kColO, va + 128 * (i & 7),
+                                                   pb + (i >> 3) * 1024 + 128 * (i & 7), idesc_pv);
+                            tc::mma_commit(pv_done(b));
                         }
+                        __syncwarp();
                     }
-                    if (jp < jq) {
-                        const int it = it0 + jp, b = it & 1;
-                        if (__all_sync(kFull, mbar_test(p_full(b), (it >> 1) & 1) &&
-                                       mbar_test(v_full(b), (it >> 1) & 1))) {
-                            tc::fence_after_sync();
-                            if (leader) {
-                                const uint64_t va = v_desc + 2048 * b, pb = p_desc + 2048 * b;
-                                if (jp > 0)
-                                    tc::mma_ss_c<true>(tmem + kColO, va, pb, idesc_pv);
-                                else
-                                    tc::mma_ss_c<false>(tmem + kColO, va, pb, idesc_pv);
+                    if (j < s.tiles) {
+                        wait(sig_full(b), par);
+                        wait(k_full(b), par);
+                        tc::fence_after_sync();
+                        if (leader) {
+                            const uint32_t d = tmem + kColS + 128 * b, ka = tmem + kColK + 64 * b;
+                            tc::mma_ts_c<false>(d, ka, q_desc, idesc_qk);
 #pragma unroll
-                                for (int i = 1; i < 8 * kTerms; ++i)
-                                    tc::mma_ss_c<true>(tmem + kColO, va + 128 * (i & 7),
-                                                       pb + (i >> 3) * 1024 + 128 * (i & 7), idesc_pv);
-                                tc::mma_commit(pv_done(b));
-                            }
-                            __syncwarp();
-                            ++jp;
-                            moved = true;
+                            for (int i = 1; i < 8 * kTerms; ++i)
+                                tc::mma_ts_c<true>(d, ka + 8 * (i & 7),
+                                                   q_desc + (i >> 3) * (kRows * 16) +
+                                                       ((i & 7) >> 2) * (kRows * 8) + (i & 3) * 2,
+                                                   idesc_qk);
+                            tc::mma_commit(s_full(b));
                         }
-                    }
-                    if (moved) {
-                        idle = 0;
-                    } else {
-                        __nanosleep(20);
-                        if (++idle > kSpinTree) {
-                            ok = false;
-                            if (lane == 0) record_status(7u);
-                        }
+                        __syncwarp();
                     }
                 }
                 it0 += s.tiles;
