@@ -64,6 +64,10 @@ constexpr int kSig = 4;                                 // tiles whose scales ar
 constexpr uint32_t kSpinTree = 1u << 22;
 constexpr float kGrow = 8.0f;                           // log2 units
 constexpr float kLowest = -1e30f;                       // running maximum before any token
+// Room left above a maximum when it is moved (log2 units), and in a new ps
+// (a factor): the next keys and V scales are often a little larger, and moving
+// costs a tile's time.
+constexpr float kHeadroom = 4.0f, kScaleRoom = 4.0f;
 // registers per thread by warpgroup: control, levels (2), softmax (4)
 // (setmaxnreg draws on what the block was launched with: the host refuses to
 // launch a build that compiled to fewer than kLaunchRegs)
@@ -302,8 +306,9 @@ __device__ __forceinline__ void soft_tile(const Soft &c, int it, bool first, int
         float rise = 0.f, nmx = 0.f;
         if (mine) {
             const float old = -ldsf(neg);
-            nmx = fmaxf(fmaxf(fmaxf(ldsf(xch), ldsf(xch + 512)), fmaxf(ldsf(xch + 1024), ldsf(xch + 1536))),
-                        old);
+            const float tm = fmaxf(fmaxf(ldsf(xch), ldsf(xch + 512)),
+                                   fmaxf(ldsf(xch + 1024), ldsf(xch + 1536)));
+            nmx = tm > old ? tm + kHeadroom : old;
             rise = nmx - old;
         }
         named_sync(4 + c.wg, 128);
@@ -566,7 +571,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
                     top = warp_redux_max(top);
                     float f = 1.f;
                     if (ps == 0.f ? top > 0.f : top * ps > 128.0f) {
-                        const float nps = pow2_floor(__fdividef(128.0f, top));
+                        const float nps = pow2_floor(__fdividef(128.0f / kScaleRoom, top));
                         f = ps == 0.f ? 1.f : pow2_ratio(nps, ps);
                         ps = nps;
                     }

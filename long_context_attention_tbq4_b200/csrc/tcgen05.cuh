@@ -159,14 +159,6 @@ __device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t lbo) 
            ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
-// The same with 64-byte swizzle (layout type 4): rows of K 64 bytes (32
-// elements along M or N) apart, in 8-row groups of 512 bytes; 16-byte chunk c
-// of row r lies at c ^ (r / 2 % 4).
-__device__ __forceinline__ uint64_t desc_mn_sw64(uint32_t saddr, uint32_t lbo) {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(lbo >> 4) << 16) |
-           ((uint64_t)(512 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)4 << 61);
-}
-
 // D f32, A and B fp16; bits 15 and 16: A, B MN-major.
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool mn_major) {
     return (1u << 4) | (mn_major ? (3u << 15) : 0u) | ((uint32_t)(N >> 3) << 17) |
