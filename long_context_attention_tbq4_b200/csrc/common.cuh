@@ -126,8 +126,10 @@ __device__ __forceinline__ float half_bits_to_float(uint16_t h) {
     return __half2float(__ushort_as_half(h));
 }
 
-// Two binary32 operations per instruction, each rounded by itself: the same
-// results as the scalar ones.
+// Two binary32 operations per instruction.  A mul2 whose result goes into an
+// add2 may be fused with it (observed: results then differ from the scalar
+// pair's in the last bit), so a sequence whose roundings are part of a
+// format takes scalar products.
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
     uint64_t r;
     asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));

@@ -165,8 +165,10 @@ __device__ __forceinline__ void encode_lane_row(const LaneRow &r, const float (&
     for (int e = 0; e < 4; ++e) {
         const uint64_t q0 = mul2(v[e], pack2(rs, rs));
         const uint64_t q = fma2(fma2(q0, pack2(-Sd, -Sd), v[e]), pack2(rs, rs), q0);
-        const uint64_t u = add2(mul2(q, pack2(7.5f, 7.5f)), pack2(7.5f, 7.5f));
         float x, y;
+        unpack2(q, x, y);
+        // a scalar product: packed, it would be fused with the sum behind it
+        const uint64_t u = add2(pack2(__fmul_rn(x, 7.5f), __fmul_rn(y, 7.5f)), pack2(7.5f, 7.5f));
         unpack2(add2(u, pack2(12582912.0f, 12582912.0f)), x, y);
         idx[2 * e] = __float_as_uint(x) & 0xFu;
         idx[2 * e + 1] = __float_as_uint(y) & 0xFu;
@@ -224,7 +226,7 @@ rope_append_kernel(const __grid_constant__ RopeParams p, int parts) {
     // y = x c + partner s, with the sign of s that the pair's formula asks for
     // (negation is exact, so this is the documented sequence of roundings); the
     // same for every head
-    uint64_t cos_a[2], sin_a[2], cos_b[2], sin_b[2];
+    float cos_a[4], sin_a[4], cos_b[4], sin_b[4];
     if constexpr (kMode != kRopeNone) {
 #pragma unroll
         for (int e = 0; e < 4; e += 2) {
@@ -232,19 +234,25 @@ rope_append_kernel(const __grid_constant__ RopeParams p, int parts) {
             if constexpr (kMode == kRopeInterleaved) {
                 x0 = x1 = cs[ta ? (ca + e) >> 1 : 0];
                 y0 = y1 = cs[tb ? (cb + e) >> 1 : 0];
-                sin_a[e / 2] = pack2(-x0.y, x0.y);
-                sin_b[e / 2] = pack2(-y0.y, y0.y);
+                sin_a[e] = -x0.y;
+                sin_a[e + 1] = x0.y;
+                sin_b[e] = -y0.y;
+                sin_b[e + 1] = y0.y;
             } else {
                 const int ia = ta ? ca + e - (fa ? 0 : half) : 0, ib = tb ? cb + e - (fb ? 0 : half) : 0;
                 x0 = cs[ia];
                 x1 = cs[ia + 1];
                 y0 = cs[ib];
                 y1 = cs[ib + 1];
-                sin_a[e / 2] = fa ? pack2(-x0.y, -x1.y) : pack2(x0.y, x1.y);
-                sin_b[e / 2] = fb ? pack2(-y0.y, -y1.y) : pack2(y0.y, y1.y);
+                sin_a[e] = fa ? -x0.y : x0.y;
+                sin_a[e + 1] = fa ? -x1.y : x1.y;
+                sin_b[e] = fb ? -y0.y : y0.y;
+                sin_b[e + 1] = fb ? -y1.y : y1.y;
             }
-            cos_a[e / 2] = pack2(x0.x, x1.x);
-            cos_b[e / 2] = pack2(y0.x, y1.x);
+            cos_a[e] = x0.x;
+            cos_a[e + 1] = x1.x;
+            cos_b[e] = y0.x;
+            cos_b[e + 1] = y1.x;
         }
     }
     // the chunks that pair with this lane's (kRopePart: read again, from cache)
@@ -261,12 +269,13 @@ rope_append_kernel(const __grid_constant__ RopeParams p, int parts) {
         }
 #pragma unroll
         for (int e = 0; e < 4; e += 2) {
+            // scalar products: a packed product and a packed sum end up fused
             float x, y;
-            unpack2(add2(mul2(pack2(r.a[e], r.a[e + 1]), cos_a[e / 2]),
-                         mul2(pack2(o.a[e], o.a[e + 1]), sin_a[e / 2])), x, y);
+            unpack2(add2(pack2(__fmul_rn(r.a[e], cos_a[e]), __fmul_rn(r.a[e + 1], cos_a[e + 1])),
+                         pack2(__fmul_rn(o.a[e], sin_a[e]), __fmul_rn(o.a[e + 1], sin_a[e + 1]))), x, y);
             if (ta) { r.a[e] = x; r.a[e + 1] = y; }
-            unpack2(add2(mul2(pack2(r.b[e], r.b[e + 1]), cos_b[e / 2]),
-                         mul2(pack2(o.b[e], o.b[e + 1]), sin_b[e / 2])), x, y);
+            unpack2(add2(pack2(__fmul_rn(r.b[e], cos_b[e]), __fmul_rn(r.b[e + 1], cos_b[e + 1])),
+                         pack2(__fmul_rn(o.b[e], sin_b[e]), __fmul_rn(o.b[e + 1], sin_b[e + 1]))), x, y);
             if (tb) { r.b[e] = x; r.b[e + 1] = y; }
         }
     };

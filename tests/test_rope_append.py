@@ -182,6 +182,28 @@ def test_far_positions(T, far):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rot,interleaved,dtype", [(128, False, "bfloat16"), (128, True, "float32"), (96, False, "float16")])
+def test_every_bit_of_many_rows(T, rot, interleaved, dtype):
+    # 24,000 rows a case: a product and a sum rounded once instead of twice
+    # changes an index in a million, and a binary32 query in ten
+    import torch
+    n, Hq, Hkv = 3000, 2, 4
+    gen = torch.Generator("cuda").manual_seed(rot + interleaved)
+    x = torch.randn((n, Hq + 2 * Hkv, 128), generator=gen, device="cuda").to(getattr(torch, dtype))
+    pos = torch.arange(n, dtype=torch.int32, device="cuda") * 37 % 200003
+    freq = _frequencies(rot, 1e6)
+    kc, vc = (torch.zeros((1, Hkv, n, 66), dtype=torch.uint8, device="cuda") for _ in "kv")
+    q = T.tbq4_rope_append(x[:, Hq: Hq + Hkv], x[:, Hq + Hkv:], torch.arange(n, dtype=torch.int32, device="cuda"),
+                           torch.from_numpy(freq).cuda(), kc, vc, q=x[:, :Hq], positions=pos,
+                           interleaved=interleaved, sign_seed=SEED)
+    rows = x.float().cpu().numpy()
+    want_q = torch.from_numpy(rope(rows[:, :Hq], pos.cpu().numpy(), freq, interleaved)).to(x.dtype)
+    assert torch.equal(q.cpu(), want_q)
+    for got, r in ((kc, rope(rows[:, Hq: Hq + Hkv], pos.cpu().numpy(), freq, interleaved)), (vc, rows[:, Hq + Hkv:])):
+        np.testing.assert_array_equal(got[0].cpu().numpy().transpose(1, 0, 2), encoded(r, SEED))
+
+
+@pytest.mark.gpu
 def test_in_place_queries_and_implied_sequences(T):
     import torch
     g = torch.Generator("cuda").manual_seed(3)
