@@ -407,13 +407,14 @@ typedef enum { TBQ4_F32 = 0, TBQ4_F16 = 1, TBQ4_BF16 = 2 } tbq4_dtype;
  *   v_cache    as tbq4_quantize_append (or pools and a block table, as
  *              tbq4_quantize_append_paged); distinct
  *   q_out      device, [n_tokens][Hq][128] of type `dtype`, 16-byte aligned;
- *              may be q itself where q has those strides
+ *              may be q itself where q has those strides, and lies over
+ *              nothing else of q, k and v
  * A token whose id is >= B, or whose slot or page lies outside the cache, has
  * no row written into the caches and flags TBQ4_ERR_CAPACITY in the device
  * status.
  * Errors: TBQ4_ERR_NULL, TBQ4_ERR_ALIGN (pointers, strides), TBQ4_ERR_SHAPE
- * (dtype, sizes, rot_dim, k_cache == v_cache), TBQ4_ERR_CAPACITY (capacity),
- * TBQ4_ERR_LAUNCH.
+ * (dtype, sizes, rot_dim, k_cache == v_cache, q_out over q, k or v),
+ * TBQ4_ERR_CAPACITY (capacity), TBQ4_ERR_LAUNCH.
  */
 TBQ4_API tbq4_status tbq4_rope_append(const void *q, int64_t q_token_stride, int64_t q_head_stride,
                                       const void *k, int64_t k_token_stride, int64_t k_head_stride,
@@ -451,7 +452,8 @@ TBQ4_API tbq4_status tbq4_rope_append_paged(
  *              calls that may overlap, or two graphs that may, need one each);
  *              its size does not depend on the lengths
  *   out        device, [B][T][Hq][128] of type out_dtype (TBQ4_F16 or
- *              TBQ4_BF16, rounded to nearest even), 16-byte aligned
+ *              TBQ4_BF16, rounded to nearest even), 16-byte aligned; may be q
+ *              itself where the two types have one size, else not over q
  * The work is divided on the device from the lengths there, so one captured
  * call serves any lengths and any number of nodes up to T.  A context below 0,
  * a count outside 0 .. T, or ctx_lens[b] + n_nodes[b] above the capacity is
@@ -461,6 +463,8 @@ TBQ4_API tbq4_status tbq4_rope_append_paged(
  * Precision: products of the cache's exact levels, sums and softmax
  * statistics in binary32; queries and softmax weights enter the tensor cores
  * as fp16 (TBQ4_BF16 outputs) or as pairs of fp16 terms (TBQ4_F16 outputs).
+ * Logits (softmax_scale q.k) of up to 2^24 in magnitude are resolved; a row
+ * with larger ones, which binary32 no longer tells apart, may come out as NaN.
  * Errors: TBQ4_ERR_NULL, TBQ4_ERR_ALIGN, TBQ4_ERR_SHAPE, TBQ4_ERR_CAPACITY,
  * TBQ4_ERR_WORKSPACE, TBQ4_ERR_LAUNCH.
  */
@@ -493,15 +497,17 @@ TBQ4_API tbq4_status tbq4_attn_tree_paged(const void *q, int q_dtype, const uint
  *   v_caches  host arrays of n_layers device pointers, each cache (or pool) as
  *             tbq4_attn_decode's and all distinct; they are read during the
  *             call only
+ *             call only.  Pages that hold ctx_lens[b] or a later slot belong to
+ *             one sequence each (a context may share full pages before them).
  *   path      device, int32 [B][max_path], 1 <= max_path <= 64
  *   n_accept  device, int32 [B], each 0 .. max_path
- *   new_lens  device, int32 [B], or NULL; not ctx_lens
+ *   new_lens  device, int32 [B], or NULL; not over ctx_lens, n_accept or path
  * A count outside 0 .. max_path, or a context that leaves no room for it,
  * moves nothing of that sequence (its new length is its old one); a node whose
  * slot or page lies outside the cache is skipped.  Both flag
  * TBQ4_ERR_CAPACITY in the device status.
  * Errors: TBQ4_ERR_NULL, TBQ4_ERR_ALIGN, TBQ4_ERR_SHAPE (sizes, a cache given
- * twice, new_lens == ctx_lens), TBQ4_ERR_CAPACITY, TBQ4_ERR_LAUNCH.
+ * twice, new_lens over an input), TBQ4_ERR_CAPACITY, TBQ4_ERR_LAUNCH.
  */
 TBQ4_API tbq4_status tbq4_tree_accept(uint8_t *const *k_caches, uint8_t *const *v_caches,
                                       int n_layers, const int32_t *ctx_lens, const int32_t *path,
@@ -517,7 +523,7 @@ TBQ4_API tbq4_status tbq4_tree_accept_paged(uint8_t *const *k_pools, uint8_t *co
 /* Profiling hook (the page has no counterpart; it serves the measurement
  * of the kernels above): while set, every attention call records `before` on its
  * stream just before its attention kernel and `after` just after it, so a
- * caller can time the attention alone with cudaEventElapsedTime.  Decode:
+ * caller can time the attention alone with cudaEventElapsedTime.  Decode, trees:
  * the events bracket the split kernel and its combine (a programmatic
  * dependent launch that starts while the split kernel drains, so the pair is
  * one region); prefill: the attention kernel alone, not its combine.  Both

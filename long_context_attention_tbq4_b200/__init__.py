@@ -361,6 +361,15 @@ def _stream_on(stream, index):
     return stream.cuda_stream
 
 
+def _empty(shape, dtype, device, stream):
+    """Memory of the stream that the call runs on: there it is free for use at
+    once, and again once this call's work is done."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _call(name, index, *args):
     """The library's function `name`, with device `index` current."""
     if index == torch.cuda.current_device():
@@ -401,7 +410,7 @@ def _rope_append(name, k, v, slots, inv_freq, kc, vc, Hkv, B, layout, index, q, 
         Hq = q.shape[1]
         qrows = _rows("q", q, dtype, index, n, Hq)
         if q_out is None:
-            q_out = torch.empty((n, Hq, D), dtype=dtype, device=q.device)
+            q_out = _empty((n, Hq, D), dtype, q.device, stream)
         else:
             _check("q_out", q_out, dtype, 3, index)
             if q_out.shape != q.shape:
@@ -427,6 +436,8 @@ def _rope_append(name, k, v, slots, inv_freq, kc, vc, Hkv, B, layout, index, q, 
         _check("inv_freq", inv_freq, torch.float64, 1, index)
         rot = 2 * inv_freq.shape[0]
         freq = inv_freq.data_ptr()
+    if n == 0:
+        return q_out                           # empty tensors have no address to pass on
     _call(name, index, *qrows, *krows, *vrows, _DTYPES[dtype], n, B, Hq, Hkv, ids, slots.data_ptr(),
           pos, freq, rot, 1 if interleaved else 0, *layout, sign_seed, kc.data_ptr(), vc.data_ptr(),
           out_ptr, _stream_on(stream, index))
@@ -476,7 +487,8 @@ def tbq4_rope_append_paged(k, v, slots, inv_freq, block_table, k_pool, v_pool, q
 def tree_mask(parents):
     """The masks of draft trees for tbq4_attn_tree: parents [T] or [B][T]
     (integers, -1 for a node that hangs off the context) -> int64 of the same
-    shape and device, bit j of node i set where j is i or an ancestor of i."""
+    shape and device, bit j of node i set where j is i or an ancestor of i.
+    Checks the parents on the host, so it is not for a graph's capture."""
     parents = torch.as_tensor(parents).long()
     T = parents.shape[-1]
     if not 1 <= T <= 64:
@@ -518,14 +530,14 @@ def _attn_tree(name, q, kc, vc, Hkv, B, cap, paged, index, ctx_lens, mask, softm
             raise ValueError(f"n_nodes must be [{B}], got {tuple(n_nodes.shape)}")
         nodes = n_nodes.data_ptr()
     if workspace is None:
-        workspace = torch.empty(max(lib.tbq4_tree_workspace_bytes(B, T, Hq, Hkv), 1),
-                                dtype=torch.uint8, device=q.device)
+        workspace = _empty(max(lib.tbq4_tree_workspace_bytes(B, T, Hq, Hkv), 1), torch.uint8, q.device,
+                           stream)
     elif not workspace.is_contiguous() or workspace.get_device() != index:
         raise ValueError(f"workspace must be contiguous, on cuda:{index}")
     if out is None:
         if out_dtype is None:
             out_dtype = torch.bfloat16 if q.dtype is torch.bfloat16 else torch.float16
-        out = torch.empty(shape, dtype=out_dtype, device=q.device)
+        out = _empty(shape, out_dtype, q.device, stream)
     elif out_dtype is not None and out.dtype is not out_dtype:
         raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
     if out.dtype not in (torch.float16, torch.bfloat16):
@@ -579,7 +591,7 @@ def _tree_accept(name, ks, vs, shape, B, cap, paged, index, ctx_lens, path, n_ac
     for t, what, ndim in ((ctx_lens, "ctx_lens", 1), (path, "path", 2), (n_accept, "n_accept", 1)):
         _check(what, t, torch.int32, ndim, index)
     if new_lens is None:
-        new_lens = torch.empty_like(ctx_lens)
+        new_lens = _empty(ctx_lens.shape, torch.int32, ctx_lens.device, stream)
     else:
         _check("new_lens", new_lens, torch.int32, 1, index)
     if not B == ctx_lens.shape[0] == path.shape[0] == n_accept.shape[0] == new_lens.shape[0]:

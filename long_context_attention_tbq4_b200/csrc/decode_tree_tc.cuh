@@ -34,14 +34,15 @@
 // maximum moves only when a logit exceeds it by 8 in log2 units: one
 // barrier-with-vote per warpgroup and tile decides that, and the rare path
 // takes the tile's maxima and rescales O (see soft_tile).  Sums stay in
-// registers until the end.  Tiles that hold drafted nodes or the end of the sequence apply masks
-// by select, to logits and to weights (a hidden block may hold anything).
+// registers until the end.  Tiles that hold drafted nodes or the end of the
+// sequence apply masks by select, to logits and to weights (a hidden block may hold anything).
 //
 // Warps (28): 0 producer (cp.async.bulk, 32-token pieces), 1 tensor-memory
 // allocation and every tcgen05.mma, 2 block scales, 4-7 and 8-11 levels (K
 // and V of the even and of the odd tiles), 12-27 softmax (four warpgroups
-// of 32 rows each; those without rows sleep until the block is done).  Every role is bound by latency
-// rather than by a unit, hence that many warps and the two level groups.
+// of 32 rows each; those without rows sleep until the block is done).  Every
+// role is bound by latency rather than by a unit, hence that many warps and
+// the two level groups.
 // The softmax waits for one barrier per tile: QK(j) is issued once levels and
 // scales of tile j are there, and its commit covers PV(j - 2), which read the
 // P' buffer that the softmax will write.
@@ -63,7 +64,7 @@ constexpr int kRawStride = kRawTile + 16;
 constexpr int kSig = 4;                                 // tiles whose scales are kept
 constexpr uint32_t kSpinTree = 1u << 22;
 constexpr float kGrow = 8.0f;                           // log2 units
-constexpr float kLowest = -1e30f;                       // running maximum before any token
+constexpr float kLowest = -3e38f;                       // running maximum before any token
 // Room left above a maximum when it is moved (log2 units), and in a new ps
 // (a factor): the next keys and V scales are often a little larger, and moving
 // costs a tile's time.
@@ -84,10 +85,10 @@ constexpr int kOffSig = kOffRawV + kRaw * kRawStride;   // S_k, S_v ps: [2][4][1
 constexpr int kOffNegM = kOffSig + 2 * kSig * kTileT * 4;  // minus the running maxima [128]
 constexpr int kOffXch = kOffNegM + 128 * 4;             // [4][128] floats
 constexpr int kOffLinv = kOffXch + 4 * 128 * 4;         // [128] floats
+constexpr int kOffFactor = kOffLinv;                    // [128] floats, before those
 constexpr int kOffVis = kOffLinv + 128 * 4;             // [64 nodes][4] words: rows that see it
 constexpr int kOffPs = kOffVis + kMaxNodes * 16;        // [4] x (factor, ps)
-constexpr int kOffMax = kOffPs + 8 * kSig;                    // [2][4] floats: V scales
-constexpr int kOffQMax = kOffMax + 32;                  // bits of the largest |q_rot|
+constexpr int kOffQMax = kOffPs + 8 * kSig;                // bits of the largest |q_rot|
 constexpr int kOffTmem = kOffQMax + 8;
 constexpr int kOffBars = kOffTmem + 8;
 constexpr int kTreeBars = 2 * kRaw + 12 + 1;
@@ -294,7 +295,7 @@ __device__ __forceinline__ void soft_tile(const Soft &c, int it, bool first, int
             tc::tmem_wait_ld();
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                const float m = warp_redux_max(sees(i, k) ? __uint_as_float(r[k]) * skc : -INFINITY);
+                const float m = warp_redux_max(sees(i, k) ? __fmul_rn(__uint_as_float(r[k]), skc) : -INFINITY);
                 if (c.lane == 8 * i + k) keep = m;
             }
         }
@@ -303,16 +304,20 @@ __device__ __forceinline__ void soft_tile(const Soft &c, int it, bool first, int
         const uint32_t xch = c.sbase + kOffXch + 4 * row, neg = c.sbase + kOffNegM + 4 * row;
         if (mine) stsf(xch + 512 * (c.t >> 5), keep);
         named_sync(4 + c.wg, 128);
-        float rise = 0.f, nmx = 0.f;
+        float f_mine = 1.f, nmx = 0.f;
         if (mine) {
             const float old = -ldsf(neg);
             const float tm = fmaxf(fmaxf(ldsf(xch), ldsf(xch + 512)),
                                    fmaxf(ldsf(xch + 1024), ldsf(xch + 1536)));
             nmx = tm > old ? tm + kHeadroom : old;
-            rise = nmx - old;
+            f_mine = nmx - old > 64.0f ? 0.f : tc::ex2(old - nmx);
         }
         named_sync(4 + c.wg, 128);
-        if (mine && c.t < 32) stsf(neg, -nmx);
+        if (mine && c.t < 32) {
+            stsf(neg, -nmx);
+            stsf(c.sbase + kOffFactor + 4 * row, f_mine);
+        }
+        named_sync(4 + c.wg, 128);
         if (!first) wait_or_fail(ok, c.bx + 8 * (8 + ((it - 1) & 1)), ((it - 1) >> 1) & 1);
         tc::fence_after_sync();
         // this token's weights once more, the sums and O by 2^-rise
@@ -322,21 +327,25 @@ __device__ __forceinline__ void soft_tile(const Soft &c, int it, bool first, int
             const uint32_t col = c.tmem + q_lane + kColO + 32 * c.wg + 8 * i;
             tc::tmem_ld8(s_col + 8 * i, r);
             if (!first) tc::tmem_ld8(col, o);
+            const uint32_t at = 128 * c.wg + 32 * i;
+            const float4 n0 = lds128f(c.sbase + kOffNegM + at), n1 = lds128f(c.sbase + kOffNegM + at + 16);
+            const float4 f0 = lds128f(c.sbase + kOffFactor + at), f1 = lds128f(c.sbase + kOffFactor + at + 16);
+            const float nm[8] = {n0.x, n0.y, n0.z, n0.w, n1.x, n1.y, n1.z, n1.w};
+            const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
             tc::tmem_wait_ld();
             float x[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                const float up = __shfl_sync(kFull, rise, 8 * i + k), f = tc::ex2(-up);
-                const float m = __shfl_sync(kFull, nmx, 8 * i + k);
-                x[k] = sees(i, k) ? tc::ex2(fmaf(__uint_as_float(r[k]), skc, -m)) : 0.f;
-                lp[8 * i + k] = up > 64.0f ? x[k] : lp[8 * i + k] * f;
-                o[k] = __float_as_uint(__uint_as_float(o[k]) * (f * fsv));
+                // the rounded product, as the maximum was taken from: unrounded, it
+                // exceeds a large maximum by more than fp16 weights allow
+                x[k] = sees(i, k) ? tc::ex2(__fadd_rn(__fmul_rn(__uint_as_float(r[k]), skc), nm[k])) : 0.f;
+                lp[8 * i + k] = f[k] == 0.f ? x[k] : lp[8 * i + k] * f[k];
+                o[k] = __float_as_uint(__uint_as_float(o[k]) * (f[k] * fsv));
             }
             if (!first) tc::tmem_st8(col, o);
             store(i, x);
         }
         tc::tmem_wait_st();
-        named_sync(4 + c.wg, 128);                                 // the new maxima are in place
     }
     fence_proxy_async();                                           // read by the tensor core
     tc::fence_before_sync();

@@ -17,6 +17,7 @@
 #include "selftest.cuh"
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <functional>
 #include <mutex>
@@ -683,6 +684,11 @@ bool elem_type(int dtype) {
     return dtype == TBQ4_F32 || dtype == TBQ4_F16 || dtype == TBQ4_BF16;
 }
 
+bool overlap(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes) {
+    const uint8_t *x = static_cast<const uint8_t *>(a), *y = static_cast<const uint8_t *>(b);
+    return x && y && x < y + b_bytes && y < x + a_bytes;
+}
+
 // A row's source: every row must start on a 16-byte boundary.
 struct Rows {
     const void *p;
@@ -690,6 +696,10 @@ struct Rows {
     bool aligned16(int dtype) const {
         const int64_t per = 16 / (int64_t)elem_bytes(dtype);
         return aligned(p, 16) && tok >= 0 && head >= 0 && tok % per == 0 && head % per == 0;
+    }
+    // bytes from the first row to the end of the last
+    int64_t extent(int n, int heads, int dtype) const {
+        return ((n - 1) * tok + (heads - 1) * head + kD) * (int64_t)elem_bytes(dtype);
     }
 };
 
@@ -725,6 +735,17 @@ tbq4_status rope_impl(const Rows &q, const Rows &k, const Rows &v, int dtype, in
         return TBQ4_ERR_SHAPE;
     if (capacity <= 0 || capacity % 8 != 0) return TBQ4_ERR_CAPACITY;
     if (n_tokens == 0) return TBQ4_OK;
+    if (Hq > 0) {
+        // warps write queries while others still read rows: nothing that they
+        // read may lie there, but for a row of q in its own place
+        const int64_t out_bytes = (int64_t)n_tokens * Hq * kD * (int64_t)elem_bytes(dtype);
+        const bool in_place = q.p == q_out && (n_tokens == 1 || q.tok == (int64_t)Hq * kD) &&
+                              (Hq == 1 || q.head == kD);
+        if ((!in_place && overlap(q.p, q.extent(n_tokens, Hq, dtype), q_out, out_bytes)) ||
+            overlap(k.p, k.extent(n_tokens, Hkv, dtype), q_out, out_bytes) ||
+            overlap(v.p, v.extent(n_tokens, Hkv, dtype), q_out, out_bytes))
+            return TBQ4_ERR_SHAPE;
+    }
     RopeParams p = {};
     p.q = q.p;
     p.k = k.p;
@@ -811,6 +832,11 @@ tbq4_status tree_impl(const void *q, int q_dtype, const uint8_t *k, const uint8_
                          Hkv;
     if (most > INT32_MAX / B) return TBQ4_ERR_SHAPE;
     if (ws_bytes < tree_ws_bytes(rows)) return TBQ4_ERR_WORKSPACE;
+    const int64_t elems = (int64_t)B * T * Hq * kD;
+    const bool in_place = q == out && elem_bytes(q_dtype) == elem_bytes(out_dtype);
+    if (!in_place && overlap(q, elems * (int64_t)elem_bytes(q_dtype), out,
+                             elems * (int64_t)elem_bytes(out_dtype)))
+        return TBQ4_ERR_SHAPE;
     tree::TreeParams p = {};
     p.q = q;
     p.q_type = q_dtype;
@@ -846,21 +872,20 @@ tbq4_status tree_impl(const void *q, int q_dtype, const uint8_t *k, const uint8_
     p.part_ml = reinterpret_cast<float2 *>(p.part_o + (size_t)2 * p.n_ctas * rows * kD);
     p.out = out;
     p.out_type = out_dtype;
-    p.out_elems = (int64_t)B * T * Hq * kD;
+    p.out_elems = elems;
     static bool attr1[64] = {}, attr2[64] = {};
     const bool two = out_dtype == TBQ4_F16;
     const void *fn = two ? (const void *)tree::tree_tc_kernel<2> : (const void *)tree::tree_tc_kernel<1>;
     if (!ensure_smem_attr(fn, tree::kTcSmem, two ? attr2 : attr1)) return TBQ4_ERR_LAUNCH;
     // the kernel moves registers between its warpgroups (setmaxnreg), which
     // is safe only from the count it was written for
-    static int regs_ok[2] = {-1, -1};
-    if (regs_ok[two] < 0) {
+    static std::atomic<int> launch_regs[2];
+    if (launch_regs[two] == 0) {
         cudaFuncAttributes fa;
-        regs_ok[two] = cudaFuncGetAttributes(&fa, fn) == cudaSuccess &&
-                       fa.numRegs >= tree::kLaunchRegs &&
-                       fa.numRegs * tree::kTcThreads <= 65536;
+        if (cudaFuncGetAttributes(&fa, fn) != cudaSuccess) return TBQ4_ERR_LAUNCH;
+        launch_regs[two] = fa.numRegs;
     }
-    if (!regs_ok[two]) return TBQ4_ERR_LAUNCH;
+    if (launch_regs[two] < tree::kLaunchRegs) return TBQ4_ERR_LAUNCH;
     cudaStream_t st = (cudaStream_t)stream;
     if (g_ev_before) cudaEventRecord(g_ev_before, st);
     if (two)
@@ -899,7 +924,9 @@ tbq4_status accept_impl(uint8_t *const *k_caches, uint8_t *const *v_caches, int 
         !aligned(new_lens, 4))
         return TBQ4_ERR_ALIGN;
     if (n_layers <= 0 || n_layers > kMaxAcceptLayers || B <= 0 || Hkv <= 0 || max_path <= 0 ||
-        max_path > kMaxPath || new_lens == ctx_lens)
+        max_path > kMaxPath || overlap(new_lens, 4 * (int64_t)B, ctx_lens, 4 * (int64_t)B) ||
+        overlap(new_lens, 4 * (int64_t)B, n_accept, 4 * (int64_t)B) ||
+        overlap(new_lens, 4 * (int64_t)B, path, 4 * (int64_t)B * max_path))
         return TBQ4_ERR_SHAPE;
     if (capacity <= 0 || capacity % 8 != 0 || capacity > INT32_MAX) return TBQ4_ERR_CAPACITY;
     const int per = std::min(n_layers, kAcceptLayers);

@@ -60,6 +60,16 @@ def test_refusals(paged):
         assert r(cap=60) == 4
 
 
+def test_refuses_queries_written_over_rows_that_are_read():
+    far = dict(k=C.c_void_p(0x100000), v=C.c_void_p(0x200000))
+    at = 4 * 4 * 128 * 2                               # bytes of q_out
+    assert _call(q=C.c_void_p(0x300000), k=C.c_void_p(0x10000 + at - 16), v=far["v"]) == 3
+    assert _call(q=C.c_void_p(0x300000), k=far["k"], v=C.c_void_p(0x10000 - 3 * 512 - 512 + 16)) == 3
+    assert _call(q=A, qs=(512, 256), **far) == 3       # q itself, but its rows lie elsewhere
+    assert _call(q=A, qs=(1024, 128), **far) == 3
+    assert _call(q=C.c_void_p(0x10000 + 256), qs=(512, 128), **far) == 3
+
+
 def test_binding_refuses_cpu_tensors(T):
     import torch
     kc = torch.zeros((1, 2, 8, 66), dtype=torch.uint8)
@@ -201,6 +211,17 @@ def test_every_bit_of_many_rows(T, rot, interleaved, dtype):
     assert torch.equal(q.cpu(), want_q)
     for got, r in ((kc, rope(rows[:, Hq: Hq + Hkv], pos.cpu().numpy(), freq, interleaved)), (vc, rows[:, Hq + Hkv:])):
         np.testing.assert_array_equal(got[0].cpu().numpy().transpose(1, 0, 2), encoded(r, SEED))
+
+
+@pytest.mark.gpu
+def test_no_tokens(T):
+    import torch
+    x = torch.zeros((0, 2, 128), device="cuda", dtype=torch.bfloat16)
+    kc, vc = (torch.full((2, 2, 8, 66), 9, dtype=torch.uint8, device="cuda") for _ in "kv")
+    q = T.tbq4_rope_append(x, x, torch.zeros(0, dtype=torch.int32, device="cuda"), None, kc, vc,
+                           q=torch.zeros((0, 4, 128), device="cuda", dtype=torch.bfloat16))
+    assert q.shape == (0, 4, 128)
+    assert bool((kc == 9).all()) and bool((vc == 9).all())
 
 
 @pytest.mark.gpu

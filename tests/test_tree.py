@@ -6,7 +6,7 @@ import ctypes as C
 import numpy as np
 import pytest
 
-from tree_helpers import check_tree, random_tree, rope, tree_attention
+from tree_helpers import check_tree, dequantised, random_tree, rope, rotation, tree_attention
 
 SEED = 5
 SCALE = 128 ** -0.5
@@ -53,6 +53,8 @@ def test_refusals(paged):
     assert r(ms=3) == 3                                # masks that overlap
     assert r(scale=float("nan")) == 3
     assert r(wb=16) == 5
+    assert r(qt=0) == 3                                # out over wider queries
+    assert r(out=C.c_void_p(0x10000 + 256)) == 3       # out over q, but not in its place
     if paged:
         assert r(table=None) == 1
         assert r(page=48) == 3
@@ -332,6 +334,90 @@ def test_same_bits_on_every_call_and_stream(T):
             got.append(call(T, s))
     torch.cuda.synchronize()
     assert all(torch.equal(ref, g) for g in got)
+
+
+@pytest.mark.gpu
+def test_memory_of_a_call_on_another_stream(T):
+    # what a call on another stream allocates must not be memory that pending
+    # work of the current stream still uses
+    import torch
+    s = make(T, 73, 1, 16, 2, 6, [9000])
+    ref = call(T, s)
+    size = T.tbq4_tree_workspace_bytes(1, 16, 12, 2)
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    held = torch.full((size,), 7, dtype=torch.uint8, device="cuda")
+    held_out = torch.full(s["q"].shape, 7, dtype=s["out"], device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)                       # some 10 ms
+    seen, seen_out = held.clone(), held_out.clone()
+    del held, held_out
+    got = call(T, s, stream=other)
+    torch.cuda.synchronize()
+    assert torch.equal(got, ref)
+    assert bool((seen == 7).all()) and bool((seen_out == 7).all())
+
+
+@pytest.mark.gpu
+def test_out_in_place_of_queries(T):
+    import torch
+    for ctx in ([2000, 3], [200000, 1]):                # whole works, and joined ones
+        s = make(T, 74, 2, 9, 2, 6, ctx)
+        want = call(T, s)
+        got = call(T, s, out=s["q"])
+        assert got.data_ptr() == s["q"].data_ptr() and torch.equal(got, want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("out", ["float16", "bfloat16"])
+def test_a_single_visible_token_of_any_logit(T, out):
+    # softmax over one token is 1 whatever the logit: rows that see themselves only
+    import torch
+    s = make(T, 75, 1, 16, 2, 3, [0], out=out, dtype="float32")
+    s["mask"] = torch.ones(16, dtype=torch.int64, device="cuda") << torch.arange(16, device="cuda")
+    s["q"] *= torch.logspace(-30, 33, 16, device="cuda")[None, :, None, None]
+    got = call(T, s)
+    v = dequantised(s["vc"][0, :, :16]) @ rotation(SEED, "cuda")       # [Hkv][16][128]
+    want = v.repeat_interleave(3, 0).transpose(0, 1)[None]
+    amp = dequantised(s["vc"][0, :, :16]).abs().sum(-1).repeat_interleave(3, 0).T[None, ..., None] / 128 ** 0.5
+    check_tree(got, want, torch.zeros_like(amp[..., 0]), amp)
+
+
+@pytest.mark.gpu
+def test_first_call_inside_a_capture():
+    # in a process of its own: nothing of the library has run before the capture
+    import subprocess
+    import sys
+    code = """
+import torch, long_context_attention_tbq4_b200 as T
+B, n, Hq, Hkv, cap = 1, 8, 12, 2, 512
+dev = dict(device="cuda")
+x = torch.randn((n, Hq + 2 * Hkv, 128), dtype=torch.bfloat16, **dev)
+ctx = torch.full((B,), 300, dtype=torch.int32, **dev)
+slots = torch.arange(300, 308, dtype=torch.int32, **dev)
+inv = 1e4 ** (-torch.arange(64, dtype=torch.float64, **dev) / 64)
+mask = torch.full((n,), 255, dtype=torch.int64, **dev)
+path = torch.tensor([[0, 3, 5]], dtype=torch.int32, **dev)
+acc = torch.tensor([3], dtype=torch.int32, **dev)
+
+def step(kc, vc):
+    q = T.tbq4_rope_append(x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], slots, inv, kc, vc, q=x[:, :Hq])
+    o = T.tbq4_attn_tree(q.view(B, n, Hq, 128), kc, vc, ctx, mask, 0.09)
+    return o, T.tbq4_tree_accept([kc], [vc], ctx, path, acc)
+
+caches = [torch.zeros((B, Hkv, cap, 66), dtype=torch.uint8, **dev) for _ in range(4)]
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    o, new = step(caches[0], caches[1])
+g.replay()
+o2, new2 = step(caches[2], caches[3])
+torch.cuda.synchronize()
+assert torch.equal(o, o2) and torch.equal(new, new2) and int(new) == 303
+assert torch.equal(caches[0], caches[2]) and torch.equal(caches[1], caches[3])
+"""
+    subprocess.run([sys.executable, "-c", code], check=True, timeout=300)
 
 
 @pytest.mark.gpu

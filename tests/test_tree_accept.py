@@ -47,6 +47,8 @@ def test_refusals(paged):
     assert r(max_path=65) == 3
     assert r(B=0) == 3
     assert r(new=A) == 3                              # the new lengths over the old ones
+    assert r(acc=0x18000, new=0x18004) == 3           # over the counts
+    assert r(path=0x18000, new=0x1801c) == 3          # over the path
     assert r(v=[A]) == 3                              # a cache given twice
     assert r(k=[A, 0x30000], v=[A2, A]) == 3
     if paged:
