@@ -254,35 +254,38 @@ __device__ __forceinline__ void soft_tile(const Soft &c, int it, bool first, int
             dmq::sts128(at + 16384, lo[0], lo[1], lo[2], lo[3]);
         }
     };
-    float top = -INFINITY;
+    // the first tile has no maxima to go by: it takes the rare path at once
+    float top = first ? INFINITY : -INFINITY;
+    if (!first) {
 #pragma unroll
-    for (int i0 = 0; i0 < kN; i0 += 2) {
-        float r[16];
-        tc::tmem_ld16(s_col + 8 * i0, r);
-        tc::tmem_wait_ld();
+        for (int i0 = 0; i0 < kN; i0 += 2) {
+            float r[16];
+            tc::tmem_ld16(s_col + 8 * i0, r);
+            tc::tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int i = i0 + e;
-            const uint32_t nega = c.sbase + kOffNegM + 128 * c.wg + 32 * i;
-            const float4 n0 = lds128f(nega), n1 = lds128f(nega + 16);
-            const float nm[8] = {n0.x, n0.y, n0.z, n0.w, n1.x, n1.y, n1.z, n1.w};
-            float x[8];                                            // log2 p: S skc - m, hidden ones -inf
+            for (int e = 0; e < 2; ++e) {
+                const int i = i0 + e;
+                const uint32_t nega = c.sbase + kOffNegM + 128 * c.wg + 32 * i;
+                const float4 n0 = lds128f(nega), n1 = lds128f(nega + 16);
+                const float nm[8] = {n0.x, n0.y, n0.z, n0.w, n1.x, n1.y, n1.z, n1.w};
+                float x[8];                                            // log2 p: S skc - m, hidden ones -inf
 #pragma unroll
-            for (int k = 0; k < 8; k += 2) {
-                unpack2(fma2(pack2(r[8 * e + k], r[8 * e + k + 1]), pack2(skc, skc),
-                             pack2(nm[k], nm[k + 1])), x[k], x[k + 1]);
-                if (!sees(i, k)) x[k] = -INFINITY;
-                if (!sees(i, k + 1)) x[k + 1] = -INFINITY;
+                for (int k = 0; k < 8; k += 2) {
+                    unpack2(fma2(pack2(r[8 * e + k], r[8 * e + k + 1]), pack2(skc, skc),
+                                 pack2(nm[k], nm[k + 1])), x[k], x[k + 1]);
+                    if (!sees(i, k)) x[k] = -INFINITY;
+                    if (!sees(i, k + 1)) x[k + 1] = -INFINITY;
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) top = fmaxf(top, x[k]);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[k] = tc::ex2(x[k]);
+#pragma unroll
+                for (int k = 0; k < 8; k += 2)
+                    unpack2(add2(pack2(lp[8 * i + k], lp[8 * i + k + 1]), pack2(x[k], x[k + 1])),
+                            lp[8 * i + k], lp[8 * i + k + 1]);
+                store(i, x);
             }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) top = fmaxf(top, x[k]);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = tc::ex2(x[k]);
-#pragma unroll
-            for (int k = 0; k < 8; k += 2)
-                unpack2(add2(pack2(lp[8 * i + k], lp[8 * i + k + 1]), pack2(x[k], x[k + 1])),
-                        lp[8 * i + k], lp[8 * i + k + 1]);
-            store(i, x);
         }
     }
     if (__builtin_expect(named_or(4 + c.wg, 128, top > kGrow || fsv != 1.f), 0)) {
