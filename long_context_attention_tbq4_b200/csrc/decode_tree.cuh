@@ -82,9 +82,10 @@ __device__ __forceinline__ int seq_blocks(const TreeParams &p, int n) {
 }
 
 // prefix[b] = units (tiles of all works) of the sequences before b, b <= B,
-// by the first warps of the CTA; every thread of the CTA calls it.  The host
-// bounds the total below 2^31.
-__device__ __forceinline__ void build_prefix(const TreeParams &p, int *prefix) {
+// every thread of the CTA calls it, and warp 0 `then` once they are there.
+// The host bounds the total below 2^31.
+template <class F>
+__device__ __forceinline__ void build_prefix(const TreeParams &p, int *prefix, F then) {
     for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
         int ctx, n;
         seq_extent(p, b, ctx, n);
@@ -108,6 +109,8 @@ __device__ __forceinline__ void build_prefix(const TreeParams &p, int *prefix) {
             base += prefix[b + 1];
             prefix[b + 1] = base;
         }
+        __syncwarp();
+        then();
     }
     __syncthreads();
 }
@@ -190,7 +193,7 @@ tree_combine_kernel(const __grid_constant__ TreeParams p) {
     __shared__ int prefix[kMaxBatch + 1];
     __shared__ float4 o_s[kJoinRows][kJoinWarps][32];
     __shared__ float2 ml_s[kJoinRows][kJoinWarps];
-    build_prefix(p, prefix);                // reads the lengths: inputs, not results
+    build_prefix(p, prefix, [] {});         // reads the lengths: inputs, not results
     // every CTA waits, also one that then has nothing to do: a kernel after
     // this one may start once this grid has ended
     asm volatile("griddepcontrol.wait;" ::: "memory");

@@ -38,7 +38,7 @@
 // sequence apply masks by select, to logits and to weights (a hidden block may hold anything).
 //
 // Warps (28): 0 producer (cp.async.bulk, 32-token pieces), 1 tensor-memory
-// allocation and every tcgen05.mma, 2 block scales, 4-7 and 8-11 levels (K
+// allocation and every tcgen05.mma, 2 block scales, 3 masks, 4-7 and 8-11 levels (K
 // and V of the even and of the odd tiles), 12-27 softmax (four warpgroups
 // of 32 rows each; those without rows sleep until the block is done).  Every
 // role is bound by latency rather than by a unit, hence that many warps and
@@ -88,7 +88,8 @@ constexpr int kOffLinv = kOffXch + 4 * 128 * 4;         // [128] floats
 constexpr int kOffFactor = kOffLinv;                    // [128] floats, before those
 constexpr int kOffVis = kOffLinv + 128 * 4;             // [64 nodes][4] words: rows that see it
 constexpr int kOffPs = kOffVis + kMaxNodes * 16;        // [4] x (factor, ps)
-constexpr int kOffQMax = kOffPs + 8 * kSig;                // bits of the largest |q_rot|
+constexpr int kOffSegment = kOffPs + 8 * kSig;           // the first Segment
+constexpr int kOffQMax = kOffSegment + 48;                // bits of the largest |q_rot|
 constexpr int kOffTmem = kOffQMax + 8;
 constexpr int kOffBars = kOffTmem + 8;
 constexpr int kTreeBars = 2 * kRaw + 12 + 1;
@@ -96,7 +97,7 @@ constexpr int kOffPrefix = kOffBars + kTreeBars * 8;
 constexpr int kTcSmem = kOffPrefix + (kMaxBatch + 1) * 4 + 1024;   // + alignment slack
 static_assert(kOffRawK % 16 == 0 && kRawStride % 16 == 0 && kOffBars % 8 == 0 && kOffVis % 16 == 0,
               "alignment");
-static_assert(kTcSmem <= 232448, "shared memory");
+static_assert(kTcSmem <= 232448 && sizeof(Segment) <= 48, "shared memory");
 
 // tensor memory columns: S (two buffers of 128), O, K levels (two of 64)
 constexpr uint32_t kColS = 0, kColO = 256, kColK = 384;
@@ -391,12 +392,6 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    int *prefix = reinterpret_cast<int *>(smem + kOffPrefix);
-    build_prefix(p, prefix);
-    const int units = prefix[p.B], shares = n_shares(p, units), cta = blockIdx.x;
-    if (cta >= shares) return;
-    const int u0 = share_begin(units, cta, shares), u1 = share_begin(units, cta + 1, shares);
-
     const uint32_t bar0 = sbase + kOffBars;
     auto raw_full = [&](int s) { return bar0 + 8 * s; };
     auto raw_empty = [&](int s) { return bar0 + 8 * (kRaw + s); };
@@ -418,7 +413,10 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
     float *tps = reinterpret_cast<float *>(smem + kOffPs);
     uint32_t *qmax = reinterpret_cast<uint32_t *>(smem + kOffQMax);
 
-    if (threadIdx.x == 0) {
+    // The allocation takes its time while the schedule is worked out.  Twenty
+    // warps that each worked out the first segment spent 3,000 cycles on it, so
+    // one does; every role finds later ones by itself, as it gets there.
+    if (threadIdx.x == 64) {
         for (int s = 0; s < kRaw; ++s) {
             mbar_init(raw_full(s), 1);
             mbar_init(raw_empty(s), 5);                 // the tile's level warps, the scales
@@ -440,15 +438,34 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
         tc::tmem_relinquish();
     }
     tc::fence_before_sync();
-    __syncthreads();
+    int *prefix = reinterpret_cast<int *>(smem + kOffPrefix);
+    Segment *first = reinterpret_cast<Segment *>(smem + kOffSegment);
+    const int cta = blockIdx.x;
+    build_prefix(p, prefix, [&] {
+        const int units = prefix[p.B], shares = n_shares(p, units);
+        if (cta >= shares) return;
+        const Segment s = segment_at(p, prefix, share_begin(units, cta, shares), share_begin(units, cta + 1, shares));
+        if (lane == 0) *first = s;
+    });
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_ptr;
+    const int units = prefix[p.B], shares = n_shares(p, units);
+    if (cta >= shares) {
+        if (warp == 1) tc::tmem_dealloc(tmem, 512);
+        return;
+    }
+    const int u0 = share_begin(units, cta, shares), u1 = share_begin(units, cta + 1, shares);
+    auto segment = [&](int u) { return u == u0 ? *first : segment_at(p, prefix, u, u1); };
 
     bool ok = true;                                     // this warp's waits have all come through
     auto wait = [&](uint32_t bar, uint32_t parity) { wait_or_fail(ok, bar, parity); };
-    // everyone but the producer and the idle warp, at the start of a segment
-    // (twice) and at its end
-    auto all_sync = [&]() { named_sync(1, 26 * 32); };
+    // Where a segment begins, the softmax warps agree among themselves, then
+    // warps 1 and 3 join them (Q and the masks are there), and again once the
+    // segment's rows are out (tensor memory and masks are free).  The other
+    // warps know tiles only, and run ahead across segments.
+    auto soft_sync = [&]() { named_sync(1, kSoftWarps * 32); };
+    auto ready_sync = [&]() { named_sync(2, (kSoftWarps + 2) * 32); };
+    auto done_sync = [&]() { named_sync(8, (kSoftWarps + 2) * 32); };
 
     if (warp < 4) {
         tc::regs_dec<kRegCtl>();
@@ -456,7 +473,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
             // ======================= producer ================================
             int it = 0;
             for (int u = u0; u < u1 && ok;) {
-                const Segment s = segment_at(p, prefix, u, u1);
+                const Segment s = segment(u);
                 u += s.tiles;
                 const int stop = s.ctx + s.n;
                 for (int j = 0; j < s.tiles; ++j, ++it) {
@@ -492,13 +509,12 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
             // ======================= MMA issuer ==============================
             int it0 = 0;
             for (int u = u0; u < u1;) {
-                const Segment s = segment_at(p, prefix, u, u1);
+                const Segment s = segment(u);
                 u += s.tiles;
                 const int N = (s.rows + 15) & ~15;
                 const uint32_t idesc_qk = tc::idesc_f16(128, N, false);
                 const uint32_t idesc_pv = tc::idesc_f16(128, N, true);
-                all_sync();
-                all_sync();
+                ready_sync();                           // Q is there
                 tc::fence_after_sync();
                 // the whole warp runs the loop, one elected lane issues
                 const bool leader = tc::elect_one();
@@ -548,7 +564,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
                     }
                 }
                 it0 += s.tiles;
-                all_sync();
+                done_sync();
             }
             if (tc::elect_one()) tc::mma_commit(drained);    // every product issued has ended
             __syncwarp();
@@ -559,12 +575,10 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
             // ======================= block scales ============================
             int it = 0;
             for (int u = u0; u < u1;) {
-                const Segment s = segment_at(p, prefix, u, u1);
+                const Segment s = segment(u);
                 u += s.tiles;
                 const int stop = s.ctx + s.n;
                 float ps = 0.f;                         // 0 until a nonzero V scale arrives
-                all_sync();
-                all_sync();
 #pragma unroll 1
                 for (int j = 0; j < s.tiles; ++j, ++it) {
                     const int st = it % kRaw, b = it & 1, sg = it & (kSig - 1);
@@ -604,7 +618,33 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
                         mbar_arrive(raw_empty(st));
                     }
                 }
-                all_sync();
+            }
+        } else {
+            // ======================= masks ===================================
+            // rows of the block that see node j, one bit each: 32 rows' masks (lane =
+            // row) transposed, 32 nodes at a time
+            for (int u = u0; u < u1;) {
+                const Segment s = segment(u);
+                u += s.tiles;
+#pragma unroll 1
+                for (int w = 0; 32 * w < s.rows; ++w) {
+                    const int c = 32 * w + lane;
+                    unsigned long long m = 0ull;
+                    if (c < s.rows) m = __ldg(p.mask + s.b * p.mask_stride + (s.row0 + c) / p.G);
+#pragma unroll
+                    for (int jh = 0; jh < 2; ++jh) {
+                        uint32_t x = (uint32_t)(m >> (32 * jh)), low = 0x0000FFFFu;
+#pragma unroll
+                        for (int k = 16; k > 0; k >>= 1) {
+                            const uint32_t y = __shfl_xor_sync(kFull, x, k);
+                            x = (lane & k) ? (x & ~low) | ((y >> k) & low) : (x & low) | ((y & low) << k);
+                            low ^= low << (k >> 1);
+                        }
+                        vis[4 * (32 * jh + lane) + w] = x;
+                    }
+                }
+                ready_sync();
+                done_sync();
             }
         }
     } else if (warp < kSoftWarp0) {
@@ -615,99 +655,72 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
         const uint32_t k_col = tmem + ((uint32_t)(t & ~31) << 16) + kColK + 64 * half;
         // 16-byte chunk c of V's row t lies at c ^ (t % 8)
         const uint32_t v_row = sbase + kOffV + 32768 * half + t * 128 + ((t & 7) << 4);
-        int it0 = 0;
-        for (int u = u0; u < u1;) {
-            const Segment s = segment_at(p, prefix, u, u1);
-            u += s.tiles;
-            if (half == 0) {
-                // rows of the block that see node j, one bit each: lane = row
-                // 32 w + lane with its node's mask, a vote per node
-                const int w = warp & 3, c = 32 * w + lane;
-                unsigned long long m = 0ull;
-                if (c < s.rows) m = __ldg(p.mask + s.b * p.mask_stride + (s.row0 + c) / p.G);
 #pragma unroll 1
-                for (int jh = 0; jh < 2; ++jh) {
-                    const uint32_t bits = (uint32_t)(m >> (32 * jh));
-                    uint32_t mine = 0;
-#pragma unroll 8
-                    for (int k = 0; k < 32; ++k) {
-                        const uint32_t v = __ballot_sync(kFull, (bits >> k) & 1u);
-                        if (lane == k) mine = v;
-                    }
-                    vis[4 * (32 * jh + lane) + w] = mine;
+        for (int it = half; it < u1 - u0; it += 2) {     // a unit is a tile
+            const int st = it % kRaw;
+            const uint32_t before = ((it >> 1) - 1) & 1;
+            wait(raw_full(st), (it / kRaw) & 1);
+            // the row's nibbles start 2 bytes behind a word boundary (even
+            // tokens) or 4 (odd ones): read from there, 32 lanes hit 32 banks
+            const uint32_t a0 = (sbase + kOffRawK + st * kRawStride + t * kBlockBytes) & ~3u;
+            const uint32_t sh = (t & 1) ? 32u : 16u;
+            if (it >= 2) wait(s_full(half), before);            // QK(it - 2) has read this buffer
+            tc::fence_after_sync();
+            // four words at a time: 32 levels, 16 columns; the next four are on
+            // their way meanwhile (reads past the row stay inside the stage)
+            const uint32_t v0 = a0 + kOffRawV - kOffRawK;
+            uint32_t w[5];
+#pragma unroll
+            for (int i = 0; i < 5; ++i) w[i] = dmq::lds32(a0 + 4 * i);
+            uint32_t ka = a0;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                uint32_t o[16], nx[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) nx[i] = dmq::lds32(ka + 20 + 4 * i);
+                ka += 16;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t l[4];
+                    word_levels(__funnelshift_rc(w[i], w[i + 1], sh), l);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[4 * i + e] = l[e];
                 }
+                tc::tmem_st16(k_col + 16 * c, o);
+                w[0] = w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i + 1] = nx[i];
             }
-            all_sync();
-            all_sync();
+#pragma unroll
+            for (int i = 0; i < 5; ++i) w[i] = dmq::lds32(v0 + 4 * i);
+            tc::tmem_wait_st();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(k_full(half));
+            if (it >= 2) wait(pv_done(half), before);
+            uint32_t va = v0;
 #pragma unroll 1
-            for (int it = it0 + ((it0 ^ half) & 1); it < it0 + s.tiles; it += 2) {
-                const int st = it % kRaw;
-                const uint32_t before = ((it >> 1) - 1) & 1;
-                wait(raw_full(st), (it / kRaw) & 1);
-                // the row's nibbles start 2 bytes behind a word boundary (even
-                // tokens) or 4 (odd ones): read from there, 32 lanes hit 32 banks
-                const uint32_t a0 = (sbase + kOffRawK + st * kRawStride + t * kBlockBytes) & ~3u;
-                const uint32_t sh = (t & 1) ? 32u : 16u;
-                if (it >= 2) wait(s_full(half), before);            // QK(it - 2) has read this buffer
-                tc::fence_after_sync();
-                // four words at a time: 32 levels, 16 columns; the next four are on
-                // their way meanwhile (reads past the row stay inside the stage)
-                const uint32_t v0 = a0 + kOffRawV - kOffRawK;
-                uint32_t w[5];
+            for (int c = 0; c < 16; c += 4, va += 16) {       // a word: eight levels, 16 bytes
+                uint32_t nx[4];
 #pragma unroll
-                for (int i = 0; i < 5; ++i) w[i] = dmq::lds32(a0 + 4 * i);
-                uint32_t ka = a0;
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t o[16], nx[4];
+                for (int i = 0; i < 4; ++i) nx[i] = dmq::lds32(va + 20 + 4 * i);
+                const uint32_t to = (v_row ^ ((c & 4) << 4)) + (c >> 3) * 16384;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) nx[i] = dmq::lds32(ka + 20 + 4 * i);
-                    ka += 16;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t l[4];
-                        word_levels(__funnelshift_rc(w[i], w[i + 1], sh), l);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) o[4 * i + e] = l[e];
-                    }
-                    tc::tmem_st16(k_col + 16 * c, o);
-                    w[0] = w[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) w[i + 1] = nx[i];
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t l[4];
+                    word_levels(__funnelshift_rc(w[i], w[i + 1], sh), l);
+                    dmq::sts128(to ^ (i << 4), l[0], l[1], l[2], l[3]);
                 }
+                w[0] = w[4];
 #pragma unroll
-                for (int i = 0; i < 5; ++i) w[i] = dmq::lds32(v0 + 4 * i);
-                tc::tmem_wait_st();
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(k_full(half));
-                if (it >= 2) wait(pv_done(half), before);
-                uint32_t va = v0;
-#pragma unroll 1
-                for (int c = 0; c < 16; c += 4, va += 16) {       // a word: eight levels, 16 bytes
-                    uint32_t nx[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) nx[i] = dmq::lds32(va + 20 + 4 * i);
-                    const uint32_t to = (v_row ^ ((c & 4) << 4)) + (c >> 3) * 16384;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t l[4];
-                        word_levels(__funnelshift_rc(w[i], w[i + 1], sh), l);
-                        dmq::sts128(to ^ (i << 4), l[0], l[1], l[2], l[3]);
-                    }
-                    w[0] = w[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) w[i + 1] = nx[i];
-                }
-                fence_proxy_async();                    // read by the tensor core
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(v_full(half));
-                    mbar_arrive(raw_empty(st));
-                }
+                for (int i = 0; i < 4; ++i) w[i + 1] = nx[i];
             }
-            it0 += s.tiles;
-            all_sync();
+            fence_proxy_async();                    // read by the tensor core
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(v_full(half));
+                mbar_arrive(raw_empty(st));
+            }
         }
     } else {
         // ======================= softmax =====================================
@@ -715,49 +728,77 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
         const int ws = warp - kSoftWarp0, wg = ws >> 2, q4 = warp & 3;
         const int t = 32 * q4 + lane;                   // token, at the end position of a dimension
         const uint32_t t_lane = tmem + ((uint32_t)(32 * q4) << 16);
-        const uint32_t sbits = lane_sign_bits(p.sign_lo, p.sign_hi, lane);
         const int wg_bar = 4 + wg;
         int it = 0;
         for (int u = u0; u < u1;) {
-            const Segment s = segment_at(p, prefix, u, u1);
+            const Segment s = segment(u);
             const bool whole = s.tiles == s.work_tiles;
             u += s.tiles;
             const int N = (s.rows + 15) & ~15, nch = N >> 3;
             // ---- queries: rotate, agree on the power of two, store -----------
-            // (rolled loops through shared memory: straight-line code that runs
-            // once per segment costs its instruction fetches, some 25 us at 16
-            // rows per warp)
-            float *stage = reinterpret_cast<float *>(smem + kOffV);   // [rows][128], no V in it yet
+            // Eight lanes per row: lane j holds channels 4 j .. 4 j + 3 of each
+            // quarter, so that only strides 4, 8 and 16 of the transform are
+            // shuffles.  (Rolled loops through shared memory: straight-line code
+            // that runs once per segment costs its instruction fetches.)
+            float *stage = reinterpret_cast<float *>(smem + kOffP);   // [rows][128], no P' in it yet
+            const int j = lane & 7;
             float mx = 0.f;
 #pragma unroll 1
-            for (int r0 = ws; r0 < s.rows; r0 += 4 * kSoftWarps) {
+            for (int r = 4 * ws + (lane >> 3); r - (lane >> 3) < s.rows; r += 4 * kSoftWarps) {
+                const int c = s.row0 + min(r, s.rows - 1);
+                const int i = c / p.G, h = s.g * p.G + (c - i * p.G);
+                const int64_t at = (((int64_t)s.b * p.T + i) * p.Hq + h) * kD + 4 * j;
+                uint64_t v[8];                          // channels (0, 1), (2, 3) of quarter k: 2 k, 2 k + 1
                 float x[4][4];
 #pragma unroll
+                for (int k = 0; k < 4; ++k) load4(p.q, p.q_type, at + 32 * k, x[k]);
+#pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const int c = s.row0 + min(r0 + kSoftWarps * k, s.rows - 1);
-                    const int i = c / p.G, h = s.g * p.G + (c - i * p.G);
-                    load4(p.q, p.q_type, (((int64_t)s.b * p.T + i) * p.Hq + h) * kD + 4 * lane, x[k]);
+                    const uint32_t sb = lane_sign_bits(p.sign_lo, p.sign_hi, j + 8 * k);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if ((sb >> e) & 1u) x[k][e] = -x[k][e];
+                    v[2 * k] = pack2(x[k][0] + x[k][1], x[k][0] - x[k][1]);
+                    v[2 * k + 1] = pack2(x[k][2] + x[k][3], x[k][2] - x[k][3]);
                 }
-#pragma unroll 1
-                for (int k = 0; k < 4; ++k) {
-                    float y[4] = {x[0][0], x[0][1], x[0][2], x[0][3]};
+                const uint64_t minus = pack2(-1.f, -1.f);
+                auto butterfly = [&](uint64_t &x, uint64_t &y) {
+                    const uint64_t sum = add2(x, y);
+                    y = fma2(y, minus, x);
+                    x = sum;
+                };
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) { x[0][e] = x[1][e]; x[1][e] = x[2][e]; x[2][e] = x[3][e]; }
-                    const int r = r0 + kSoftWarps * k;
-                    if (r >= s.rows) break;
-                    warp_rotate128(y, sbits, lane);
+                for (int k = 0; k < 8; k += 2) butterfly(v[k], v[k + 1]);               // stride 2
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float a = fabsf(y[e]);
-                        if (isfinite(a)) mx = fmaxf(mx, a);
+                for (int m = 1; m < 8; m <<= 1) {                                       // 4, 8, 16
+                    const float neg = (j & m) ? -1.f : 1.f;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        float lo, hi;
+                        unpack2(v[k], lo, hi);
+                        v[k] = fma2(v[k], pack2(neg, neg), pack2(__shfl_xor_sync(kFull, lo, m),
+                                                                 __shfl_xor_sync(kFull, hi, m)));
                     }
-                    *reinterpret_cast<float4 *>(stage + r * kD + 4 * lane) = make_float4(y[0], y[1], y[2], y[3]);
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k)                                             // 32, 64
+                    if (!(k & 2)) butterfly(v[k], v[k + 2]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) butterfly(v[k], v[k + 4]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float4 y;
+                    unpack2(mul2(v[2 * k], pack2(rot_c(), rot_c())), y.x, y.y);
+                    unpack2(mul2(v[2 * k + 1], pack2(rot_c(), rot_c())), y.z, y.w);
+                    const float top = fmaxf(fmaxf(fabsf(y.x), fabsf(y.y)), fmaxf(fabsf(y.z), fabsf(y.w)));
+                    if (isfinite(y.x) && isfinite(y.y) && isfinite(y.z) && isfinite(y.w)) mx = fmaxf(mx, top);
+                    if (r < s.rows) *reinterpret_cast<float4 *>(stage + r * kD + 4 * j + 32 * k) = y;
                 }
             }
             mx = warp_max(mx);
             if (lane == 0 && mx > 0.f) atomicMax(qmax, __float_as_uint(mx));
             for (int r = ws * 32 + lane; r < kRows; r += 32 * kSoftWarps) negm[r] = -kLowest;
-            all_sync();
+            soft_sync();
             const float big = __uint_as_float(*qmax);
             int e2 = 0;
             if (big > 0.f) frexpf(big, &e2);            // big < 2^e2
@@ -765,38 +806,34 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
             const float up = ldexpf(1.0f, 15 - e2);
             // log2 logit = S skc with skc = S_k c (levels are (2n - 15) 2^-11)
             const float c2 = p.scale * (1.4426950408889634f * 2048.0f / 15.0f) * ldexpf(1.0f, e2 - 15);
+            // 16 lanes per row, eight dimensions each
 #pragma unroll 1
-            for (int r = ws; r < N; r += kSoftWarps) {
-                // the operands' order of dimensions: pairs (d, d + 4) of each eight
-                const bool odd = lane & 1;
-                float x[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int r = 2 * ws + (lane >> 4); r < N; r += 2 * kSoftWarps) {
+                const int ch = lane & 15;
+                float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
                 if (r < s.rows) {
-                    const float4 y = *reinterpret_cast<const float4 *>(stage + r * kD + 4 * lane);
-                    x[0] = y.x * up;
-                    x[1] = y.y * up;
-                    x[2] = y.z * up;
-                    x[3] = y.w * up;
+                    a = *reinterpret_cast<const float4 *>(stage + r * kD + 8 * ch);
+                    b = *reinterpret_cast<const float4 *>(stage + r * kD + 8 * ch + 4);
                 }
-                const float g0 = __shfl_xor_sync(kFull, odd ? x[0] : x[2], 1);
-                const float g1 = __shfl_xor_sync(kFull, odd ? x[1] : x[3], 1);
-                const float a0 = odd ? g0 : x[0], b0 = odd ? x[2] : g0;
-                const float a1 = odd ? g1 : x[1], b1 = odd ? x[3] : g1;
-                const int ch = lane >> 1;
+                const float x[8] = {a.x * up, b.x * up, a.y * up, b.y * up,     // the operands' order
+                                    a.z * up, b.z * up, a.w * up, b.w * up};
                 const uint32_t at = sbase + kOffQ + (ch >> 3) * (kRows * 128) + (r >> 3) * 1024 +
-                                    (r & 7) * 128 + (((ch & 7) ^ (r & 7)) << 4) + (odd ? 8 : 0);
-                const __half2 h0 = __floats2half2_rn(a0, b0), h1 = __floats2half2_rn(a1, b1);
-                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at),
-                             "r"(*reinterpret_cast<const uint32_t *>(&h0)),
-                             "r"(*reinterpret_cast<const uint32_t *>(&h1)) : "memory");
+                                    (r & 7) * 128 + (((ch & 7) ^ (r & 7)) << 4);
+                uint32_t h[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) h[k] = half2_bits(x[2 * k], x[2 * k + 1]);
+                dmq::sts128(at, h[0], h[1], h[2], h[3]);
                 if constexpr (kTerms == 2) {
-                    const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
-                    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + kRows * 256),
-                                 "r"(half2_bits(a0 - f0.x, b0 - f0.y)),
-                                 "r"(half2_bits(a1 - f1.x, b1 - f1.y)) : "memory");
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[k]));
+                        h[k] = half2_bits(x[2 * k] - f.x, x[2 * k + 1] - f.y);
+                    }
+                    dmq::sts128(at + kRows * 256, h[0], h[1], h[2], h[3]);
                 }
             }
             fence_proxy_async();                        // read by the tensor core
-            all_sync();
+            ready_sync();
             if (ws == 0 && lane == 0) *qmax = 0u;       // for the next segment (read before the barrier)
 
             const Soft sc = {sbase, tmem, bx, t, lane, wg, kPArrivals / 4 / ((nch + 3) >> 2), c2};
@@ -827,7 +864,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
             const int d = dim_at(t);
             float *po = p.part_o + (int64_t)part_slot(s, cta) * p.rows * kD;
 #pragma unroll 1
-            for (int c = 4 * wg; c < min(nch, 4 * wg + 4); ++c) {   // (V is done with its buffers)
+            for (int c = 4 * wg; c < min(nch, 4 * wg + 4); ++c) {   // (P' is done with its buffers)
                 uint32_t o[8];
                 tc::tmem_ld8(t_lane + kColO + 8 * c, o);
                 tc::tmem_wait_ld();
@@ -847,7 +884,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
                     store_out(p, s.b, s.g, s.row0 + r, v, lane);
                 }
             }
-            all_sync();
+            done_sync();
         }
     }
 }
