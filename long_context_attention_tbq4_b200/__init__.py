@@ -11,6 +11,8 @@ blocks inside its inner loop (trefon.com, "Kontekst 262K na jednej RTX 4090:
 co dodalem do llama.cpp-turboq", section "Od czego zaczalem").
 """
 import ctypes as C
+from array import array
+from operator import attrgetter
 
 import numpy as np
 import torch
@@ -339,6 +341,11 @@ _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}    # tbq4_dtyp
 # The calls below serve single decode steps, so the host's share counts: a
 # check reads each attribute once, and devices are compared by index.
 
+_dtype_of, _shape_of = attrgetter("dtype"), attrgetter("shape")
+# the current stream's handle without a Stream object around it (1.2 us)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+
 def _check(name, t, dtype, ndim, index):
     """A contiguous CUDA tensor of this type and rank on device `index`."""
     if not (t.dtype is dtype and t.dim() == ndim and t.is_contiguous() and t.get_device() == index):
@@ -355,19 +362,19 @@ def _device_index(t, name):
 
 def _stream_on(stream, index):
     if stream is None:
-        return torch.cuda.current_stream(index).cuda_stream
+        return _raw_stream(index)
     if stream.device.index != index:
         raise ValueError(f"stream on {stream.device}, tensors on cuda:{index}")
     return stream.cuda_stream
 
 
-def _empty(shape, dtype, device, stream):
+def _empty(like, shape, dtype, stream):
     """Memory of the stream that the call runs on: there it is free for use at
     once, and again once this call's work is done."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
 
 
 def _call(name, index, *args):
@@ -410,7 +417,7 @@ def _rope_append(name, k, v, slots, inv_freq, kc, vc, Hkv, B, layout, index, q, 
         Hq = q.shape[1]
         qrows = _rows("q", q, dtype, index, n, Hq)
         if q_out is None:
-            q_out = _empty((n, Hq, D), dtype, q.device, stream)
+            q_out = _empty(q, (n, Hq, D), dtype, stream)
         else:
             _check("q_out", q_out, dtype, 3, index)
             if q_out.shape != q.shape:
@@ -530,14 +537,13 @@ def _attn_tree(name, q, kc, vc, Hkv, B, cap, paged, index, ctx_lens, mask, softm
             raise ValueError(f"n_nodes must be [{B}], got {tuple(n_nodes.shape)}")
         nodes = n_nodes.data_ptr()
     if workspace is None:
-        workspace = _empty(max(lib.tbq4_tree_workspace_bytes(B, T, Hq, Hkv), 1), torch.uint8, q.device,
-                           stream)
+        workspace = _empty(q, (max(lib.tbq4_tree_workspace_bytes(B, T, Hq, Hkv), 1),), torch.uint8, stream)
     elif not workspace.is_contiguous() or workspace.get_device() != index:
         raise ValueError(f"workspace must be contiguous, on cuda:{index}")
     if out is None:
         if out_dtype is None:
             out_dtype = torch.bfloat16 if q.dtype is torch.bfloat16 else torch.float16
-        out = _empty(shape, out_dtype, q.device, stream)
+        out = _empty(q, shape, out_dtype, stream)
     elif out_dtype is not None and out.dtype is not out_dtype:
         raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
     if out.dtype not in (torch.float16, torch.bfloat16):
@@ -580,24 +586,28 @@ def tbq4_attn_tree_paged(q, k_pool, v_pool, block_table, ctx_lens, tree_mask, so
 
 
 def _tree_accept(name, ks, vs, shape, B, cap, paged, index, ctx_lens, path, n_accept, new_lens, stream):
-    n = len(ks)
-    if n != len(vs):
-        raise ValueError(f"{n} K and {len(vs)} V caches: as many of each")
-    u8 = torch.uint8
-    for c in (*ks, *vs):
-        if not (c.dtype is u8 and c.shape == shape and c.is_contiguous() and c.get_device() == index):
-            _check("each cache", c, u8, 4, index)
-            raise ValueError("the caches differ in shape")
+    n, caches = len(ks), [*ks, *vs]
+    if len(caches) != 2 * n:
+        raise ValueError(f"{n} K and {len(caches) - n} V caches: as many of each")
+    # in bulk: a loop over the 56 caches of 28 layers took longer than the kernel
+    if not (set(map(torch.Tensor.get_device, caches)) == {index}
+            and all(map(torch.Tensor.is_contiguous, caches))
+            and set(map(_dtype_of, caches)) == {torch.uint8}
+            and list(map(_shape_of, caches)).count(shape) == 2 * n):
+        for c in caches:
+            _check("each cache", c, torch.uint8, 4, index)
+        raise ValueError("the caches differ in shape")
     for t, what, ndim in ((ctx_lens, "ctx_lens", 1), (path, "path", 2), (n_accept, "n_accept", 1)):
         _check(what, t, torch.int32, ndim, index)
     if new_lens is None:
-        new_lens = _empty(ctx_lens.shape, torch.int32, ctx_lens.device, stream)
+        new_lens = _empty(ctx_lens, ctx_lens.shape, torch.int32, stream)
     else:
         _check("new_lens", new_lens, torch.int32, 1, index)
     if not B == ctx_lens.shape[0] == path.shape[0] == n_accept.shape[0] == new_lens.shape[0]:
         raise ValueError("shape mismatch between caches, ctx_lens, path, n_accept and new_lens")
-    ptrs = C.c_void_p * n
-    _call(name, index, ptrs(*[c.data_ptr() for c in ks]), ptrs(*[c.data_ptr() for c in vs]), n, *paged,
+    ptrs = array("Q", map(torch.Tensor.data_ptr, caches))
+    at = ptrs.buffer_info()[0]
+    _call(name, index, at, at + 8 * n, n, *paged,
           ctx_lens.data_ptr(), path.data_ptr(), n_accept.data_ptr(), path.shape[1], B, shape[1], *cap,
           new_lens.data_ptr(), _stream_on(stream, index))
     return new_lens
