@@ -193,16 +193,13 @@ tree_combine_kernel(const __grid_constant__ TreeParams p) {
     __shared__ int prefix[kMaxBatch + 1];
     __shared__ float4 o_s[kJoinRows][kJoinWarps][32];
     __shared__ float2 ml_s[kJoinRows][kJoinWarps];
-    build_prefix(p, prefix, [] {});         // reads the lengths: inputs, not results
-    // every CTA waits, also one that then has nothing to do: a kernel after
-    // this one may start once this grid has ended
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // the schedule follows from the lengths: inputs, not results of the kernel
+    // before, so it is worked out while that one still runs
+    build_prefix(p, prefix, [] {});
     const int units = prefix[p.B], shares = n_shares(p, units);
-    int u;                                  // a unit of the work
+    int u = -1;                             // a unit of the work
     if (p.join_starts) {
-        const int c1 = blockIdx.x + 1;
-        if (c1 >= shares) return;
-        u = share_begin(units, c1, shares);
+        if ((int)blockIdx.x + 1 < shares) u = share_begin(units, blockIdx.x + 1, shares);
     } else {
         const int most = (p.T * p.G + p.rows - 1) / p.rows;        // blocks of a sequence, at most
         const int blk = blockIdx.x % most, bg = blockIdx.x / most;
@@ -210,13 +207,19 @@ tree_combine_kernel(const __grid_constant__ TreeParams p) {
         int ctx, n;
         seq_extent(p, b, ctx, n);
         const int blocks = seq_blocks(p, n);
-        if (blk >= blocks) return;
-        u = prefix[b] + (g * blocks + blk) * seq_tiles(ctx, n);
+        if (blk < blocks) u = prefix[b] + (g * blocks + blk) * seq_tiles(ctx, n);
     }
-    const Segment s = segment_at(p, prefix, u, units);
-    const int first = share_of(units, s.begin, shares);
-    const int last = share_of(units, s.begin + s.work_tiles - 1, shares);
-    if (first == last) return;              // whole: its CTA wrote the rows
+    Segment s = {};
+    int first = 0, last = 0;
+    if (u >= 0) {
+        s = segment_at(p, prefix, u, units);
+        first = share_of(units, s.begin, shares);
+        last = share_of(units, s.begin + s.work_tiles - 1, shares);
+    }
+    // every CTA waits, also one that then has nothing to do: a kernel after
+    // this one may start once this grid has ended
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (first == last) return;              // none, or whole: its CTA wrote the rows
     if (p.join_starts && (u == s.begin || first != (int)blockIdx.x)) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int sub = warp % kJoinWarps, ri = warp / kJoinWarps;
