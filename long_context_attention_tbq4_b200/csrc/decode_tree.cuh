@@ -184,15 +184,21 @@ __device__ __forceinline__ void store_out(const TreeParams &p, int b, int g, int
 // the first such start, owns the work.  Either way at most one CTA column per
 // split work does anything (walking the starts of 148 shares for the four
 // works of one sequence took 17 to 39 us, mostly CTAs that found nothing).
-// Four warps per row take every fourth partial with a running maximum, and
-// the four results meet in shared memory.
-constexpr int kJoinWarps = 4, kJoinRows = 4;
+// A CTA's warps share the work's partials: four warps per row where it has
+// more than kJoinMany, else one, and rows in turn.  A warp takes its partials'
+// maxima and sums first, a lane each, then the rows, kJoinBatch in flight; the
+// warps of a row meet in shared memory.  (Four warps throughout: 8 trees of 25
+// nodes 236 us instead of 224; one throughout: 5 nodes at 262K 83 instead of
+// 79.  A running maximum over partials read one by one cost 10 us more on the
+// long sequences.)
+constexpr int kJoinWarps = 16, kJoinMany = 16, kJoinBatch = 8;
+static_assert(kJoinMany <= 64 && (kNumSMs + 3) / 4 + 1 <= 64, "two partials a lane");
 
-__global__ void __launch_bounds__(kJoinWarps * kJoinRows * 32)
+__global__ void __launch_bounds__(kJoinWarps * 32)
 tree_combine_kernel(const __grid_constant__ TreeParams p) {
     __shared__ int prefix[kMaxBatch + 1];
-    __shared__ float4 o_s[kJoinRows][kJoinWarps][32];
-    __shared__ float2 ml_s[kJoinRows][kJoinWarps];
+    __shared__ float4 o_s[kJoinWarps][32];
+    __shared__ float2 ml_s[kJoinWarps];
     // the schedule follows from the lengths: inputs, not results of the kernel
     // before, so it is worked out while that one still runs
     build_prefix(p, prefix, [] {});
@@ -222,52 +228,79 @@ tree_combine_kernel(const __grid_constant__ TreeParams p) {
     if (first == last) return;              // none, or whole: its CTA wrote the rows
     if (p.join_starts && (u == s.begin || first != (int)blockIdx.x)) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int sub = warp % kJoinWarps, ri = warp / kJoinWarps;
-    const int r = blockIdx.y * kJoinRows + ri;
-    if ((int)blockIdx.y * kJoinRows >= s.rows) return;
-    float M = -INFINITY, L = 0.f;
-    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r < s.rows) {
-#pragma unroll 4
-        for (int c = first + sub; c <= last; c += kJoinWarps) {
-            const int64_t row = (int64_t)(2 * c + (c == first)) * p.rows + r;
-            const float2 ml = __ldcg(p.part_ml + row);
-            const float4 o = __ldcg(reinterpret_cast<const float4 *>(p.part_o + row * kD) + lane);
-            if (ml.y == 0.f) continue;      // the run's tokens are all invisible to this row
-            const float Mn = fmaxf(M, ml.x);
-            const float a = exp2f(M - Mn), w = exp2f(ml.x - Mn);
-            O.x = O.x * a + o.x * w;
-            O.y = O.y * a + o.y * w;
-            O.z = O.z * a + o.z * w;
-            O.w = O.w * a + o.w * w;
-            L = L * a + ml.y * w;
-            M = Mn;
+    const int per = last - first >= kJoinMany ? 4 : 1;              // warps per row
+    const int sub = warp & (per - 1), step = kJoinWarps / per;
+    for (int r0 = blockIdx.y * step; r0 < s.rows; r0 += gridDim.y * step) {
+        const int r = r0 + warp / per;
+        float M = -INFINITY, L = 0.f;
+        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < s.rows) {
+            // this warp's partials are k = 0 .. n - 1; lane l holds (m, l) of l and l + 32
+            const int c0 = first + sub, n = c0 <= last ? (last - c0) / per + 1 : 0;
+            auto row_of = [&](int k) {
+                const int c = c0 + per * k;
+                return (int64_t)(2 * c + (c == first)) * p.rows + r;
+            };
+            float2 ml[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                ml[h] = lane + 32 * h < n ? __ldcg(p.part_ml + row_of(lane + 32 * h)) : make_float2(0.f, 0.f);
+            float w[2] = {};
+#pragma unroll 1
+            for (int k0 = 0; k0 < n; k0 += kJoinBatch) {
+                float4 o[kJoinBatch];
+#pragma unroll
+                for (int k = 0; k < kJoinBatch; ++k)
+                    if (k0 + k < n)
+                        o[k] = __ldcg(reinterpret_cast<const float4 *>(p.part_o + row_of(k0 + k) * kD) + lane);
+                if (k0 == 0) {              // a sum of 0: the run's tokens are all invisible to this row
+                    M = warp_max(fmaxf(ml[0].y == 0.f ? -INFINITY : ml[0].x,
+                                       ml[1].y == 0.f ? -INFINITY : ml[1].x));
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) w[h] = ml[h].y == 0.f ? 0.f : exp2f(ml[h].x - M);
+                    L = warp_sum(w[0] * ml[0].y + w[1] * ml[1].y);
+                }
+#pragma unroll
+                for (int k = 0; k < kJoinBatch; ++k) {
+                    const float f = __shfl_sync(kFull, k0 + k < 32 ? w[0] : w[1], (k0 + k) & 31);
+                    if (k0 + k >= n) break;
+                    O.x += f * o[k].x;
+                    O.y += f * o[k].y;
+                    O.z += f * o[k].z;
+                    O.w += f * o[k].w;
+                }
+            }
         }
+        float v[4] = {O.x, O.y, O.z, O.w};
+        if (per > 1) {
+            o_s[warp][lane] = O;
+            if (lane == 0) ml_s[warp] = make_float2(M, L);
+            __syncthreads();
+            if (sub == 0) {
+                float Mt = M, f[4];
+#pragma unroll
+                for (int w = 1; w < 4; ++w) Mt = fmaxf(Mt, ml_s[warp + w].x);
+                L = v[0] = v[1] = v[2] = v[3] = 0.f;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const float2 ml = ml_s[warp + w];
+                    const float4 o = o_s[warp + w][lane];
+                    f[w] = ml.y == 0.f ? 0.f : exp2f(ml.x - Mt);
+                    v[0] += f[w] * o.x;
+                    v[1] += f[w] * o.y;
+                    v[2] += f[w] * o.z;
+                    v[3] += f[w] * o.w;
+                    L += f[w] * ml.y;
+                }
+            }
+            __syncthreads();                // o_s is free for the next rows
+        }
+        if (sub != 0 || r >= s.rows) continue;
+        const float inv = L == 0.f ? 0.f : 1.0f / L;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] *= inv;
+        store_out(p, s.b, s.g, s.row0 + r, v, lane);
     }
-    o_s[ri][sub][lane] = O;
-    if (lane == 0) ml_s[ri][sub] = make_float2(M, L);
-    __syncthreads();
-    if (sub != 0 || r >= s.rows) return;
-    float Mt = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) Mt = fmaxf(Mt, ml_s[ri][w].x);
-    float v[4] = {0.f, 0.f, 0.f, 0.f}, Lt = 0.f;
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) {
-        const float2 ml = ml_s[ri][w];
-        if (ml.y == 0.f) continue;
-        const float f = exp2f(ml.x - Mt);
-        const float4 o = o_s[ri][w][lane];
-        v[0] += f * o.x;
-        v[1] += f * o.y;
-        v[2] += f * o.z;
-        v[3] += f * o.w;
-        Lt += f * ml.y;
-    }
-    const float inv = Lt == 0.f ? 0.f : 1.0f / Lt;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] *= inv;
-    store_out(p, s.b, s.g, s.row0 + r, v, lane);
 }
 
 // Byte offset of 32-token piece `t` (a multiple of 32) of (b, g) in either

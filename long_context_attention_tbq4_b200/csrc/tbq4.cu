@@ -895,9 +895,12 @@ tbq4_status tree_impl(const void *q, int q_dtype, const uint8_t *k, const uint8_
     // the join, a programmatic dependent launch: one CTA per work (or start of
     // a share, when there are more works than shares) and group of rows
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(p.join_starts ? p.n_ctas - 1 : works),
-                       (unsigned)ceil_div(std::min(rows, T * p.G), tree::kJoinRows));
-    cfg.blockDim = dim3(tree::kJoinWarps * tree::kJoinRows * 32);
+    // one CTA per SM, or one per four rows if those are fewer (four per SM: 64
+    // nodes at 262K 248 us instead of 241, 8 trees of 25 nodes 229 instead of 223)
+    const int columns = (int)(p.join_starts ? p.n_ctas - 1 : works);
+    cfg.gridDim = dim3((unsigned)columns, (unsigned)std::min<int64_t>(ceil_div(std::min(rows, T * p.G), 4),
+                                                                      ceil_div(kNumSMs, columns)));
+    cfg.blockDim = dim3(tree::kJoinWarps * 32);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
