@@ -192,7 +192,6 @@ __device__ __forceinline__ void store_out(const TreeParams &p, int b, int g, int
 // 79.  A running maximum over partials read one by one cost 10 us more on the
 // long sequences.)
 constexpr int kJoinWarps = 16, kJoinMany = 16, kJoinBatch = 8;
-static_assert(kJoinMany <= 64 && (kNumSMs + 3) / 4 + 1 <= 64, "two partials a lane");
 
 __global__ void __launch_bounds__(kJoinWarps * 32)
 tree_combine_kernel(const __grid_constant__ TreeParams p) {

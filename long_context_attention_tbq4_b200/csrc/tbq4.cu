@@ -901,6 +901,7 @@ tbq4_status tree_impl(const void *q, int q_dtype, const uint8_t *k, const uint8_
     cfg.gridDim = dim3((unsigned)columns, (unsigned)std::min<int64_t>(ceil_div(std::min(rows, T * p.G), 4),
                                                                       ceil_div(kNumSMs, columns)));
     cfg.blockDim = dim3(tree::kJoinWarps * 32);
+    static_assert(tree::kJoinMany <= 64 && kNumSMs / 4 + 1 <= 64, "two partials a lane");
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
