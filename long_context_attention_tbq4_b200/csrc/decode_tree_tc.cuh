@@ -35,12 +35,14 @@
 // barrier-with-vote per warpgroup and tile decides that, and the rare path
 // takes the tile's maxima and rescales O (see soft_tile).  Sums stay in
 // registers until the end.  Tiles that hold drafted nodes or the end of the
-// sequence apply masks by select, to logits and to weights (a hidden block may hold anything).
+// sequence apply masks by select, to logits and to weights (a hidden block may
+// hold anything).
 //
 // Warps (28): 0 producer (cp.async.bulk, 32-token pieces), 1 tensor-memory
-// allocation and every tcgen05.mma, 2 block scales, 3 masks, 4-7 and 8-11 levels (K
-// and V of the even and of the odd tiles), 12-27 softmax (four warpgroups
-// of 32 rows each; those without rows sleep until the block is done).  Every
+// allocation and every tcgen05.mma, 2 block scales, 3 masks, 4-7 and 8-11
+// levels (K and V of the even and of the odd tiles), 12-27 softmax (four
+// warpgroups of 32 rows each; those without rows sleep until the block is
+// done).  Every
 // role is bound by latency rather than by a unit, hence that many warps and
 // the two level groups.
 // The softmax waits for one barrier per tile: QK(j) is issued once levels and

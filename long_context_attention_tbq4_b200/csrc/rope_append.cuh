@@ -180,7 +180,7 @@ __device__ __forceinline__ void encode_lane_row(const LaneRow &r, const float (&
 // A warp takes a token, or, where there are few, every `parts`-th pair of
 // rows of one: its cosines and sines into shared memory (32 lanes, up to two
 // each), then pair after pair of its Hq + 2 Hkv rows.  Bound by issue and by
-// the latency of its loads: 16,384 tokens of 24/4 heads in bf16 take 62.5 us
+// the latency of its loads: 16,384 tokens of 24/4 heads in bf16 take 62.6 us
 // (3.9 TB/s; the copy rate would allow 37 us), 117 us with one row per warp
 // and the token's angles behind a block barrier.  Seven blocks of four warps
 // per SM: eight spill, six hide less (82 us with four pairs in flight).
