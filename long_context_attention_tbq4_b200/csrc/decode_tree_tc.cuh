@@ -42,9 +42,8 @@
 // allocation and every tcgen05.mma, 2 block scales, 3 masks, 4-7 and 8-11
 // levels (K and V of the even and of the odd tiles), 12-27 softmax (four
 // warpgroups of 32 rows each; those without rows sleep until the block is
-// done).  Every
-// role is bound by latency rather than by a unit, hence that many warps and
-// the two level groups.
+// done).  Every role is bound by latency rather than by a unit, hence that many
+// warps and the two level groups.
 // The softmax waits for one barrier per tile: QK(j) is issued once levels and
 // scales of tile j are there, and its commit covers PV(j - 2), which read the
 // P' buffer that the softmax will write.
@@ -94,7 +93,7 @@ constexpr int kOffSegment = kOffPs + 8 * kSig;           // the first Segment
 constexpr int kOffQMax = kOffSegment + 48;                // bits of the largest |q_rot|
 constexpr int kOffTmem = kOffQMax + 8;
 constexpr int kOffBars = kOffTmem + 8;
-constexpr int kTreeBars = 2 * kRaw + 12 + 1;
+constexpr int kTreeBars = 2 * kRaw + 10 + 1;
 constexpr int kOffPrefix = kOffBars + kTreeBars * 8;
 constexpr int kTcSmem = kOffPrefix + (kMaxBatch + 1) * 4 + 1024;   // + alignment slack
 static_assert(kOffRawK % 16 == 0 && kRawStride % 16 == 0 && kOffBars % 8 == 0 && kOffVis % 16 == 0,
@@ -398,13 +397,12 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
     auto raw_full = [&](int s) { return bar0 + 8 * s; };
     auto raw_empty = [&](int s) { return bar0 + 8 * (kRaw + s); };
     const uint32_t bx = bar0 + 8 * 2 * kRaw;
-    auto k_full = [&](int b) { return bx + 8 * b; };            // K levels -> MMA
+    auto k_full = [&](int b) { return bx + 8 * b; };            // K levels, scales -> MMA
     auto s_full = [&](int b) { return bx + 8 * (2 + b); };      // S ready (K levels read)
     auto v_full = [&](int b) { return bx + 8 * (6 + b); };      // V levels -> MMA
     auto p_full = [&](int b) { return bx + 8 * (4 + b); };      // P' -> MMA; S and the scales read
     auto pv_done = [&](int b) { return bx + 8 * (8 + b); };     // V levels and P' read
-    auto sig_full = [&](int b) { return bx + 8 * (10 + b); };   // scales -> MMA
-    const uint32_t drained = bx + 8 * 12;
+    const uint32_t drained = bx + 8 * 10;
     uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(smem + kOffTmem);
     float *sig_k = reinterpret_cast<float *>(smem + kOffSig);       // [4][128]
     float *sig_v = sig_k + kSig * kTileT;                           // [4][128]
@@ -424,12 +422,11 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
             mbar_init(raw_empty(s), 5);                 // the tile's level warps, the scales
         }
         for (int b = 0; b < 2; ++b) {
-            mbar_init(k_full(b), 4);
+            mbar_init(k_full(b), 5);                    // four warps' levels, the scales
             mbar_init(s_full(b), 1);
             mbar_init(v_full(b), 4);
             mbar_init(p_full(b), kPArrivals);
             mbar_init(pv_done(b), 1);
-            mbar_init(sig_full(b), 1);
         }
         mbar_init(drained, 1);
         *qmax = 0u;
@@ -548,7 +545,6 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
                         __syncwarp();
                     }
                     if (j < s.tiles) {
-                        wait(sig_full(b), par);
                         wait(k_full(b), par);
                         tc::fence_after_sync();
                         if (leader) {
@@ -616,7 +612,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
                     }
                     __syncwarp();
                     if (lane == 0) {
-                        mbar_arrive(sig_full(b));
+                        mbar_arrive(k_full(b));
                         mbar_arrive(raw_empty(st));
                     }
                 }
