@@ -119,7 +119,9 @@ __device__ __forceinline__ void build_prefix(const TreeParams &p, int *prefix, F
 // c, and the share that holds unit u.
 __device__ __forceinline__ int n_shares(const TreeParams &p, int units) { return min(p.n_ctas, units); }
 __device__ __forceinline__ int share_begin(int units, int c, int shares) {
-    return (int)((int64_t)units * c / shares);
+    // units c / shares; the remainder's product is small (shares^2)
+    const int each = units / shares, rest = units - each * shares;
+    return each * c + rest * c / shares;
 }
 __device__ __forceinline__ int share_of(int units, int u, int shares) {
     return (int)((((int64_t)u + 1) * shares - 1) / units);

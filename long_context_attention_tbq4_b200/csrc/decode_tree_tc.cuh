@@ -89,8 +89,8 @@ constexpr int kOffLinv = kOffXch + 4 * 128 * 4;         // [128] floats
 constexpr int kOffFactor = kOffLinv;                    // [128] floats, before those
 constexpr int kOffVis = kOffLinv + 128 * 4;             // [64 nodes][4] words: rows that see it
 constexpr int kOffPs = kOffVis + kMaxNodes * 16;        // [4] x (factor, ps)
-constexpr int kOffSegment = kOffPs + 8 * kSig;           // the first Segment
-constexpr int kOffQMax = kOffSegment + 48;                // bits of the largest |q_rot|
+constexpr int kOffSegment = kOffPs + 8 * kSig;           // the first Segment, the CTA's units
+constexpr int kOffQMax = kOffSegment + 56;                // bits of the largest |q_rot|
 constexpr int kOffTmem = kOffQMax + 8;
 constexpr int kOffBars = kOffTmem + 8;
 constexpr int kTreeBars = 2 * kRaw + 10 + 1;
@@ -98,7 +98,7 @@ constexpr int kOffPrefix = kOffBars + kTreeBars * 8;
 constexpr int kTcSmem = kOffPrefix + (kMaxBatch + 1) * 4 + 1024;   // + alignment slack
 static_assert(kOffRawK % 16 == 0 && kRawStride % 16 == 0 && kOffBars % 8 == 0 && kOffVis % 16 == 0,
               "alignment");
-static_assert(kTcSmem <= 232448 && sizeof(Segment) <= 48, "shared memory");
+static_assert(kTcSmem <= 232448 && sizeof(Segment) + 8 <= 56, "shared memory");
 
 // tensor memory columns: S (two buffers of 128), O, K levels (two of 64)
 constexpr uint32_t kColS = 0, kColO = 256, kColK = 384;
@@ -439,21 +439,30 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
     tc::fence_before_sync();
     int *prefix = reinterpret_cast<int *>(smem + kOffPrefix);
     Segment *first = reinterpret_cast<Segment *>(smem + kOffSegment);
+    int *range = reinterpret_cast<int *>(first + 1);    // first and last unit + 1
     const int cta = blockIdx.x;
     build_prefix(p, prefix, [&] {
         const int units = prefix[p.B], shares = n_shares(p, units);
-        if (cta >= shares) return;
-        const Segment s = segment_at(p, prefix, share_begin(units, cta, shares), share_begin(units, cta + 1, shares));
-        if (lane == 0) *first = s;
+        Segment s = {};
+        int u0 = 0, u1 = 0;
+        if (cta < shares) {
+            u0 = share_begin(units, cta, shares);
+            u1 = share_begin(units, cta + 1, shares);
+            s = segment_at(p, prefix, u0, u1);
+        }
+        if (lane == 0) {
+            *first = s;
+            range[0] = u0;
+            range[1] = u1;
+        }
     });
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_ptr;
-    const int units = prefix[p.B], shares = n_shares(p, units);
-    if (cta >= shares) {
+    const int u0 = range[0], u1 = range[1];
+    if (u0 == u1) {                                     // more CTAs than units
         if (warp == 1) tc::tmem_dealloc(tmem, 512);
         return;
     }
-    const int u0 = share_begin(units, cta, shares), u1 = share_begin(units, cta + 1, shares);
     auto segment = [&](int u) { return u == u0 ? *first : segment_at(p, prefix, u, u1); };
 
     bool ok = true;                                     // this warp's waits have all come through
