@@ -21,17 +21,18 @@
 //         channel below 2^15: 28 binades of rows below the largest keep all
 //         11 bits.  kTerms = 2 adds the remainder as a second fp16 term.
 //   P'    p S_v ps, thread = token writes eight rows per 16-byte store
-//         (MN-major).  ps is the power of two that keeps S_v ps <= 2^7 for
-//         every V scale seen so far (p <= 2^8): most weights stay normal fp16
-//         numbers.  When it shrinks, O moves with it.  kTerms = 2 adds the
-//         remainder as a second term.
+//         (MN-major).  ps is the power of two that keeps S_v ps <= 2^9 for
+//         every V scale seen so far (p <= 2^6): fp16's range is for the rows
+//         whose tokens all have small V scales, which keep 2^-28 of the
+//         largest weight times the largest scale.  When ps shrinks, O moves
+//         with it.  kTerms = 2 adds the remainder as a second term.
 // One term rounds a query or a weight by up to 2^-11 relative, a tenth of a
 // bf16 output's own rounding; fp16 outputs, which that would double, take two
 // terms (22 bits) and blocks of 64 rows in the same shared memory.
 //
 // Softmax.  thread = token, so its S_k and S_v are scalars and a row's
 // running maximum is one number for all threads (shared memory).  The
-// maximum moves only when a logit exceeds it by 8 in log2 units: one
+// maximum moves only when a logit exceeds it by 6 in log2 units: one
 // barrier-with-vote per warpgroup and tile decides that, and the rare path
 // takes the tile's maxima and rescales O (see soft_tile).  Sums stay in
 // registers until the end.  Tiles that hold drafted nodes or the end of the
@@ -64,7 +65,10 @@ constexpr int kRawTile = kTileT * kBlockBytes;          // 8448
 constexpr int kRawStride = kRawTile + 16;
 constexpr int kSig = 4;                                 // tiles whose scales are kept
 constexpr uint32_t kSpinTree = 1u << 22;
-constexpr float kGrow = 8.0f;                           // log2 units
+// Growth that a row's maximum is left behind by (log2 units), and the largest
+// S_v ps: 2^kGrow kMaxScale is in fp16's range.  8 and 128 take 1 % less time at
+// 64 nodes, 4 and 2048 take 3 % more.
+constexpr float kGrow = 6.0f, kMaxScale = 512.0f;
 constexpr float kLowest = -3e38f;                       // running maximum before any token
 // Room left above a maximum when it is moved (log2 units), and in a new ps
 // (a factor): the next keys and V scales are often a little larger, and moving
@@ -204,7 +208,7 @@ struct Soft {
 // One tile for kN chunks of 8 rows (rows 32 wg + 8 i ..).  The weights are
 // taken with the running maxima as they are, stored, and only then does the
 // warpgroup vote on whether a logit exceeded its maximum by more than kGrow
-// (a weight above 2^8, which fp16 may not hold): the rare tile that did is
+// (a weight above 2^6, which fp16 may not hold): the rare tile that did is
 // stored again with the new maxima.  The sums take that without a second
 // pass: fp32 holds weights of up to 2^127, so they are scaled afterwards, and
 // where a maximum rose by more than 64 the old sum no longer counts.  (Voting
@@ -603,8 +607,8 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
                     }
                     top = warp_redux_max(top);
                     float f = 1.f;
-                    if (ps == 0.f ? top > 0.f : top * ps > 128.0f) {
-                        const float nps = pow2_floor(__fdividef(128.0f / kScaleRoom, top));
+                    if (ps == 0.f ? top > 0.f : top * ps > kMaxScale) {
+                        const float nps = pow2_floor(__fdividef(kMaxScale / kScaleRoom, top));
                         f = ps == 0.f ? 1.f : pow2_ratio(nps, ps);
                         ps = nps;
                     }
