@@ -10,22 +10,28 @@
 // Tokens are the rows of S^T and dimensions the rows of O^T, so the width of
 // both products is the number of query rows: a small tree pays for its own
 // rows only.  Operands:
-//   K, V  levels (2n - 15) 2^-11, exact in fp16 (nibbles masked into
+//   K     levels (2n - 15) 2^-11, exact in fp16 (nibbles masked into
 //         subnormals, one HFMA2); the block scales stay out of the products.
 //         A word of nibbles gives eight levels in the order 0 4 1 5 2 6 3 7,
 //         which is the order of the dimensions in every operand here.  K goes
-//         from registers to tensor memory, thread = token = lane; V goes to
-//         shared memory as it lies, token by token, and enters as the
+//         from registers to tensor memory, thread = token = lane.
+//   V     levels times the power of two of their block's scale, S_v = m 2^e
+//         with m in [1, 2): (2n - 15) 2^(e-7), exact in fp16 for every e (-14
+//         .. 15; smaller scales are subnormal and keep e = -14, m < 1).  V goes
+//         to shared memory as it lies, token by token, and enters as the
 //         MN-major operand (no transposition anywhere).
 //   Q     q_rot times a power of two that brings the block's largest finite
 //         channel below 2^15: 28 binades of rows below the largest keep all
 //         11 bits.  kTerms = 2 adds the remainder as a second fp16 term.
-//   P'    p S_v ps, thread = token writes eight rows per 16-byte store
-//         (MN-major).  ps is the power of two that keeps S_v ps <= 2^9 for
-//         every V scale seen so far (p <= 2^6): fp16's range is for the rows
-//         whose tokens all have small V scales, which keep 2^-28 of the
-//         largest weight times the largest scale.  When ps shrinks, O moves
-//         with it.  kTerms = 2 adds the remainder as a second term.
+//   P'    p m 2^8 <= 2^15 (p <= 2^6), thread = token writes eight rows per
+//         16-byte store (MN-major).  The scale's power of two lies in V's
+//         levels, so what a weight is rounded to depends on its own row and
+//         token only: 2^-11 relative, or 2^-25 where P' is subnormal.  A row's
+//         largest weight is at least 2^-4 (kHeadroom), so that is 2^-29 of the
+//         row's largest weight (times S_v, or 2^-14 if that is more).  (One
+//         power of two for all tokens, from the largest V scale among them, had
+//         rows lose bits to tokens that their mask hid.)  kTerms = 2 adds the
+//         remainder as a second term.
 // One term rounds a query or a weight by up to 2^-11 relative, a tenth of a
 // bf16 output's own rounding; fp16 outputs, which that would double, take two
 // terms (22 bits) and blocks of 64 rows in the same shared memory.
@@ -65,15 +71,14 @@ constexpr int kRawTile = kTileT * kBlockBytes;          // 8448
 constexpr int kRawStride = kRawTile + 16;
 constexpr int kSig = 4;                                 // tiles whose scales are kept
 constexpr uint32_t kSpinTree = 1u << 22;
-// Growth that a row's maximum is left behind by (log2 units), and the largest
-// S_v ps: 2^kGrow kMaxScale is in fp16's range.  8 and 128 take 1 % less time at
-// 64 nodes, 4 and 2048 take 3 % more.
-constexpr float kGrow = 6.0f, kMaxScale = 512.0f;
+// Growth that a row's maximum is left behind by (log2 units), and the power of
+// two of P': 2^(kGrow + 1 + kPShift) is in fp16's range.
+constexpr float kGrow = 6.0f;
+constexpr int kPShift = 8;
 constexpr float kLowest = -3e38f;                       // running maximum before any token
-// Room left above a maximum when it is moved (log2 units), and in a new ps
-// (a factor): the next keys and V scales are often a little larger, and moving
-// costs a tile's time.
-constexpr float kHeadroom = 4.0f, kScaleRoom = 4.0f;
+// Room left above a maximum when it is moved (log2 units): the next keys are
+// often a little larger, and moving costs a tile's time.
+constexpr float kHeadroom = 4.0f;
 // registers per thread by warpgroup: control, levels (2), softmax (4)
 // (setmaxnreg draws on what the block was launched with: the host refuses to
 // launch a build that compiled to fewer than kLaunchRegs)
@@ -86,14 +91,13 @@ constexpr int kOffP = 32768;                            // 2 x 32 KB: kTerms x r
 constexpr int kOffV = kOffP + 2 * 32768;                // 2 x 32 KB
 constexpr int kOffRawK = kOffV + 2 * 32768;
 constexpr int kOffRawV = kOffRawK + kRaw * kRawStride;
-constexpr int kOffSig = kOffRawV + kRaw * kRawStride;   // S_k, S_v ps: [2][4][128] floats
+constexpr int kOffSig = kOffRawV + kRaw * kRawStride;   // S_k, m 2^kPShift: [2][4][128] floats
 constexpr int kOffNegM = kOffSig + 2 * kSig * kTileT * 4;  // minus the running maxima [128]
 constexpr int kOffXch = kOffNegM + 128 * 4;             // [4][128] floats
 constexpr int kOffLinv = kOffXch + 4 * 128 * 4;         // [128] floats
 constexpr int kOffFactor = kOffLinv;                    // [128] floats, before those
 constexpr int kOffVis = kOffLinv + 128 * 4;             // [64 nodes][4] words: rows that see it
-constexpr int kOffPs = kOffVis + kMaxNodes * 16;        // [4] x (factor, ps)
-constexpr int kOffSegment = kOffPs + 8 * kSig;           // the first Segment, the CTA's units
+constexpr int kOffSegment = kOffVis + kMaxNodes * 16;   // the first Segment, the CTA's units
 constexpr int kOffQMax = kOffSegment + 56;                // bits of the largest |q_rot|
 constexpr int kOffTmem = kOffQMax + 8;
 constexpr int kOffBars = kOffTmem + 8;
@@ -138,6 +142,22 @@ __device__ __forceinline__ void word_levels(uint32_t w, uint32_t (&o)[4]) {
     o[1] = dmq::vhi(w);
     o[2] = dmq::vlo(w >> 8);
     o[3] = dmq::vhi(w >> 8);
+}
+// The same nibbles as (2n - 15) 2^(e-7) for a block scale's power of two 2^e,
+// given as its fp16 bits twice: with n moved into the mantissa of 1 + n / 64,
+// that is 2^e (1 + n / 64) - 143 2^(e-7), one HFMA2 with exact operands.
+__device__ __forceinline__ void word_levels_scaled(uint32_t w, uint32_t pow2, uint32_t (&o)[4]) {
+    const uint32_t less = pow2 | 0x80788078u;             // -143 2^(e-7)
+    auto level = [&](uint32_t x) { return dmq::hfma2u((x & 0x00F000F0u) | 0x3C003C00u, pow2, less); };
+    o[0] = level(w << 4);
+    o[1] = level(w);
+    o[2] = level(w >> 4);
+    o[3] = level(w >> 8);
+}
+// Exponent field of a block scale's power of two: at least that of 2^-14, and
+// finite also where the scale is not.
+__device__ __forceinline__ uint32_t scale_field(uint32_t half_bits) {
+    return min(max((half_bits >> 10) & 31u, 1u), 30u);
 }
 // Dimension at position `pos` of an operand: the order above, by eights.
 __device__ __forceinline__ int dim_at(int pos) {
@@ -224,8 +244,7 @@ __device__ __forceinline__ void soft_tile(const Soft &c, int it, bool first, int
     const uint32_t q_lane = (uint32_t)(c.t & ~31) << 16;
     const uint32_t s_col = c.tmem + q_lane + kColS + 128 * b + 32 * c.wg;
     const float skc = ldsf(c.sbase + kOffSig + (kTileT * sg + c.t) * 4) * c.c2;
-    const float svp = ldsf(c.sbase + kOffSig + (kTileT * (kSig + sg) + c.t) * 4);
-    const float fsv = ldsf(c.sbase + kOffPs + 8 * sg);
+    const float m8 = ldsf(c.sbase + kOffSig + (kTileT * (kSig + sg) + c.t) * 4);
     uint32_t see = 0xFFFFFFFFu;                                    // rows that see this token
     if (kMasked && node >= 0)
         see = node < n_nodes ? dmq::lds32(c.sbase + kOffVis + 16 * node + 4 * c.wg) : 0u;
@@ -234,12 +253,12 @@ __device__ __forceinline__ void soft_tile(const Soft &c, int it, bool first, int
     // 4 (wg % 2) + i of the 64-row atom wg / 2
     const uint32_t pt = c.sbase + kOffP + 32768 * b + (c.wg >> 1) * 16384 + c.t * 128 +
                         ((((c.wg & 1) << 2) ^ (c.t & 7)) << 4);
-    // P' = p S_v ps of chunk i
+    // P' = p m 2^8 of chunk i
     auto store = [&](int i, const float (&pr)[8]) {
         float y[8];
 #pragma unroll
         for (int k = 0; k < 8; k += 2) {
-            unpack2(mul2(pack2(pr[k], pr[k + 1]), pack2(svp, svp)), y[k], y[k + 1]);
+            unpack2(mul2(pack2(pr[k], pr[k + 1]), pack2(m8, m8)), y[k], y[k + 1]);
             if constexpr (kMasked) {                               // a hidden block may hold anything
                 if (!sees(i, k)) y[k] = 0.f;
                 if (!sees(i, k + 1)) y[k + 1] = 0.f;
@@ -294,7 +313,7 @@ __device__ __forceinline__ void soft_tile(const Soft &c, int it, bool first, int
             }
         }
     }
-    if (__builtin_expect(named_or(4 + c.wg, 128, top > kGrow || fsv != 1.f), 0)) {
+    if (__builtin_expect(named_or(4 + c.wg, 128, top > kGrow), 0)) {
         // move the maxima to the tile's; lane 8 i + k stands for row k of chunk i
         float keep = kLowest;
 #pragma unroll
@@ -349,7 +368,7 @@ __device__ __forceinline__ void soft_tile(const Soft &c, int it, bool first, int
                 // exceeds a large maximum by more than fp16 weights allow
                 x[k] = sees(i, k) ? tc::ex2(__fadd_rn(__fmul_rn(__uint_as_float(r[k]), skc), nm[k])) : 0.f;
                 lp[8 * i + k] = f[k] == 0.f ? x[k] : lp[8 * i + k] * f[k];
-                o[k] = __float_as_uint(__uint_as_float(o[k]) * (f[k] * fsv));
+                o[k] = __float_as_uint(__uint_as_float(o[k]) * f[k]);
             }
             if (!first) tc::tmem_st8(col, o);
             store(i, x);
@@ -414,7 +433,6 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
     float *xch = reinterpret_cast<float *>(smem + kOffXch);
     float *linv = reinterpret_cast<float *>(smem + kOffLinv);
     uint32_t *vis = reinterpret_cast<uint32_t *>(smem + kOffVis);
-    float *tps = reinterpret_cast<float *>(smem + kOffPs);
     uint32_t *qmax = reinterpret_cast<uint32_t *>(smem + kOffQMax);
 
     // The allocation takes its time while the schedule is worked out.  Twenty
@@ -588,40 +606,26 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
             for (int u = u0; u < u1;) {
                 const Segment s = segment(u);
                 u += s.tiles;
-                const int stop = s.ctx + s.n;
-                float ps = 0.f;                         // 0 until a nonzero V scale arrives
 #pragma unroll 1
                 for (int j = 0; j < s.tiles; ++j, ++it) {
                     const int st = it % kRaw, b = it & 1, sg = it & (kSig - 1);
                     wait(raw_full(st), (it / kRaw) & 1);
                     const uint32_t row = sbase + kOffRawK + st * kRawStride + lane * kBlockBytes;
-                    const int left = stop - (s.tile0 + j) * kTileT - lane;    // tokens from this one on
-                    float sk[4], sv[4], top = 0.f;
+                    float sk[4], m8[4];                 // S_k, and m 2^8 of S_v = m 2^e
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const uint32_t at = row + 32 * i * kBlockBytes;
                         sk[i] = half_bits_to_float((uint16_t)dmq::lds16(at));
-                        sv[i] = half_bits_to_float((uint16_t)dmq::lds16(at + kOffRawV - kOffRawK));
-                        if (left <= 32 * i) sv[i] = 0.f;
-                        if (isfinite(sv[i])) top = fmaxf(top, sv[i]);
-                    }
-                    top = warp_redux_max(top);
-                    float f = 1.f;
-                    if (ps == 0.f ? top > 0.f : top * ps > kMaxScale) {
-                        const float nps = pow2_floor(__fdividef(kMaxScale / kScaleRoom, top));
-                        f = ps == 0.f ? 1.f : pow2_ratio(nps, ps);
-                        ps = nps;
+                        const uint32_t sv = dmq::lds16(at + kOffRawV - kOffRawK);
+                        m8[i] = half_bits_to_float((uint16_t)sv) *
+                                __uint_as_float((142u + kPShift - scale_field(sv)) << 23);
                     }
                     // QK(it - 2) was issued after the softmax had read tile it - 4's
                     if (it >= 2) wait(s_full(b), ((it >> 1) - 1) & 1);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         sig_k[kTileT * sg + 32 * i + lane] = sk[i];
-                        sig_v[kTileT * sg + 32 * i + lane] = sv[i] * ps;
-                    }
-                    if (lane == 0) {
-                        tps[2 * sg] = f;
-                        tps[2 * sg + 1] = ps;
+                        sig_v[kTileT * sg + 32 * i + lane] = m8[i];
                     }
                     __syncwarp();
                     if (lane == 0) {
@@ -709,7 +713,9 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
             __syncwarp();
             if (lane == 0) mbar_arrive(k_full(half));
             if (it >= 2) wait(pv_done(half), before);
+            // the scale lies in front of the first nibbles, in the word's other half
             uint32_t va = v0;
+            const uint32_t pow2 = scale_field(w[0] >> (sh - 16)) * 0x04000400u;
 #pragma unroll 1
             for (int c = 0; c < 16; c += 4, va += 16) {       // a word: eight levels, 16 bytes
                 uint32_t nx[4];
@@ -719,7 +725,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     uint32_t l[4];
-                    word_levels(__funnelshift_rc(w[i], w[i + 1], sh), l);
+                    word_levels_scaled(__funnelshift_rc(w[i], w[i + 1], sh), pow2, l);
                     dmq::sts128(to ^ (i << 4), l[0], l[1], l[2], l[3]);
                 }
                 w[0] = w[4];
@@ -860,9 +866,8 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
             const int last = it - 1;
             wait(pv_done(last & 1), (last >> 1) & 1);
             tc::fence_after_sync();
-            const float ps = tps[2 * (last & (kSig - 1)) + 1];
-            // sum_t P'_t (2n - 15) 2^-11 -> sum_t p S_v (2n - 15) / 15
-            const float back = (ps > 0.f ? pow2_inv(ps) : 1.0f) * (2048.0f / 15.0f);
+            // sum_t p m 2^8 (2n - 15) 2^(e-7) -> sum_t p S_v (2n - 15) / 15
+            constexpr float back = 128.0f / (15 << kPShift);
             named_sync(wg_bar, 128);
             const int row = 32 * wg + t;
             if (t < 32 && row < s.rows) {
