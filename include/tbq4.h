@@ -463,8 +463,9 @@ TBQ4_API tbq4_status tbq4_rope_append_paged(
  * Precision: products of the cache's exact levels, sums and softmax
  * statistics in binary32; queries and softmax weights enter the tensor cores
  * as fp16 (TBQ4_BF16 outputs) or as pairs of fp16 terms (TBQ4_F16 outputs).
- * A term's rounding is 2^-11 relative; below that a weight is held to 2^-29 of
- * its row's largest weight, or finer (a V scale S below 2^-14: to 2^-43 / S).
+ * One term's rounding is 2^-11 relative, a pair's 2^-22; below that a weight is
+ * held to 2^-29 of its row's largest weight, a pair to 2^-40, or finer (for V
+ * scales S below 2^-14, 2^-14 / S times that).
  * What a row's mask hides, and the V scales of other tokens, have no part in it.
  * Logits (softmax_scale q.k) of up to 2^24 in magnitude are resolved; a row
  * with larger ones, which binary32 no longer tells apart, may come out as NaN.

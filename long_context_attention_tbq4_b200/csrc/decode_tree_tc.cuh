@@ -31,7 +31,10 @@
 //         row's largest weight (times S_v, or 2^-14 if that is more).  (One
 //         power of two for all tokens, from the largest V scale among them, had
 //         rows lose bits to tokens that their mask hid.)  kTerms = 2 adds the
-//         remainder as a second term.
+//         remainder as a second term, times 2^11 and with an accumulator of its
+//         own: 2^-22 relative, or 2^-40 of the row's largest weight.  (Added to
+//         O itself, the remainder is subnormal where P' < 2^-3: 32,767 tokens
+//         20 below a token without V, which make the row, were 6 % off.)
 // One term rounds a query or a weight by up to 2^-11 relative, a tenth of a
 // bf16 output's own rounding; fp16 outputs, which that would double, take two
 // terms (22 bits) and blocks of 64 rows in the same shared memory.
@@ -109,7 +112,9 @@ static_assert(kOffRawK % 16 == 0 && kRawStride % 16 == 0 && kOffBars % 8 == 0 &&
 static_assert(kTcSmem <= 232448 && sizeof(Segment) + 8 <= 56, "shared memory");
 
 // tensor memory columns: S (two buffers of 128), O, K levels (two of 64)
-constexpr uint32_t kColS = 0, kColO = 256, kColK = 384;
+// (kTerms = 2: S takes 64 columns, and the remainders' O those behind it)
+constexpr uint32_t kColS = 0, kColO = 256, kColK = 384, kColO2 = 64;
+constexpr float kLowTerm = 2048.0f;
 
 __device__ __forceinline__ void named_sync(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -274,7 +279,7 @@ __device__ __forceinline__ void soft_tile(const Soft &c, int it, bool first, int
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[k]));
-                lo[k] = half2_bits(y[2 * k] - f.x, y[2 * k + 1] - f.y);
+                lo[k] = half2_bits((y[2 * k] - f.x) * kLowTerm, (y[2 * k + 1] - f.y) * kLowTerm);
             }
             dmq::sts128(at + 16384, lo[0], lo[1], lo[2], lo[3]);
         }
@@ -372,6 +377,24 @@ __device__ __forceinline__ void soft_tile(const Soft &c, int it, bool first, int
             }
             if (!first) tc::tmem_st8(col, o);
             store(i, x);
+        }
+        if constexpr (kTerms == 2) {
+            if (!first) {
+                // a rolled loop of its own: inside the one above, the spills that it
+                // brings reach the frequent path (5 nodes at 262K 153 us instead of 76)
+#pragma unroll 1
+                for (int i = 0; i < kN; ++i) {
+                    uint32_t o[8];
+                    const uint32_t col = c.tmem + q_lane + kColO2 + 32 * c.wg + 8 * i;
+                    tc::tmem_ld8(col, o);
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        o[k] = __float_as_uint(__uint_as_float(o[k]) *
+                                               ldsf(c.sbase + kOffFactor + 128 * c.wg + 32 * i + 4 * k));
+                    tc::tmem_st8(col, o);
+                }
+            }
         }
         tc::tmem_wait_st();
     }
@@ -563,14 +586,17 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
                         tc::fence_after_sync();
                         if (leader) {
                             const uint64_t va = v_desc + 2048 * b, pb = p_desc + 2048 * b;
-                            if (j > 2)
-                                tc::mma_ss_c<true>(tmem + kColO, va, pb, idesc_pv);
-                            else
-                                tc::mma_ss_c<false>(tmem + kColO, va, pb, idesc_pv);
 #pragma unroll
-                            for (int i = 1; i < 8 * kTerms; ++i)         // descriptors count 16 bytes
-                                tc::mma_ss_c<true>(tmem + kColO, va + 128 * (i & 7),
-                                                   pb + (i >> 3) * 1024 + 128 * (i & 7), idesc_pv);
+                            for (int e = 0; e < kTerms; ++e) {           // descriptors count 16 bytes
+                                const uint32_t d = tmem + (e ? kColO2 : kColO);
+                                if (j > 2)
+                                    tc::mma_ss_c<true>(d, va, pb + 1024 * e, idesc_pv);
+                                else
+                                    tc::mma_ss_c<false>(d, va, pb + 1024 * e, idesc_pv);
+#pragma unroll
+                                for (int i = 1; i < 8; ++i)
+                                    tc::mma_ss_c<true>(d, va + 128 * i, pb + 1024 * e + 128 * i, idesc_pv);
+                            }
                             tc::mma_commit(pv_done(b));
                         }
                         __syncwarp();
@@ -884,6 +910,14 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
                 uint32_t o[8];
                 tc::tmem_ld8(t_lane + kColO + 8 * c, o);
                 tc::tmem_wait_ld();
+                if constexpr (kTerms == 2) {
+                    uint32_t lo[8];
+                    tc::tmem_ld8(t_lane + kColO2 + 8 * c, lo);
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        o[k] = __float_as_uint(__uint_as_float(o[k]) + __uint_as_float(lo[k]) * (1.0f / kLowTerm));
+                }
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     const int row = 8 * c + k;

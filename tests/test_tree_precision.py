@@ -47,3 +47,34 @@ def test_a_token_of_the_largest_scale_and_no_weight(T, out):  # noqa: F811
     s["vc"][..., :2] = sv.half().view(torch.uint8)
     s["vc"][:, :, 3, :2] = _bits(0x7BFF)
     check(T, s)
+
+
+@pytest.mark.gpu
+def test_many_small_weights_beside_a_large_one(T):  # noqa: F811
+    # 32,767 tokens 20 below a token whose V is nearly 0: each weight is 2^-29
+    # of the row's largest, and they make the row.  160 sequences share the
+    # pages, so that CTAs hold whole sequences (a share of the tokens without
+    # the large one would be easy)
+    import torch
+    from tree_helpers import check_tree, tree_attention
+    n, B = 32767, 160
+    gen = torch.Generator("cuda").manual_seed(83)
+    q = torch.randn((1, 1, 1, 128), generator=gen, device="cuda")
+    k = torch.randn((1, n + 1, 1, 128), generator=gen, device="cuda")
+    k[0, 0, 0] = 20.0 * 128 ** 0.5 * q[0, 0, 0] / (q ** 2).sum()
+    v = 100.0 + torch.randn((1, n + 1, 1, 128), generator=gen, device="cuda")
+    v[0, 0] = 1e-6
+    table = torch.arange(128, dtype=torch.int32, device="cuda")[None]
+    s = dict(kc=torch.empty((128, 1, 256, 66), dtype=torch.uint8, device="cuda"), table=table.expand(B, 128).contiguous(),
+             q=q.expand(B, 1, 1, 128).contiguous(), out=torch.float16,
+             ctx=torch.full((B,), n, dtype=torch.int32, device="cuda"),
+             n=torch.ones(B, dtype=torch.int32, device="cuda"),
+             mask=torch.ones(1, dtype=torch.int64, device="cuda"))
+    s["vc"] = torch.empty_like(s["kc"])
+    start = torch.zeros(1, dtype=torch.int32, device="cuda")
+    T.tbq4_quantize_append_paged(k, start, table, s["kc"], 5)
+    T.tbq4_quantize_append_paged(v, start, table, s["vc"], 5)
+    got = call(T, s)
+    want, eps, amp = tree_attention(q, s["kc"], s["vc"], s["ctx"], s["n"], s["mask"], 128 ** -0.5, 5, table)
+    assert T.tbq4_get_device_status() == 0
+    check_tree(got, want.expand(B, 1, 1, 128), eps.expand(B, 1, 1), amp.expand(B, 1, 1, 1))
