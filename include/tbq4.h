@@ -466,7 +466,9 @@ TBQ4_API tbq4_status tbq4_rope_append_paged(
  * One term's rounding is 2^-11 relative, a pair's 2^-22; below that a weight is
  * held to 2^-29 of its row's largest weight, a pair to 2^-40, or finer (for V
  * scales S below 2^-14, 2^-14 / S times that).
- * What a row's mask hides, and the V scales of other tokens, have no part in it.
+ * A rotated query channel is held to 2^-25 of its own row's largest, or finer.
+ * What a row's mask hides, the V scales of other tokens and the queries of other
+ * rows have no part in it.
  * Logits (softmax_scale q.k) of up to 2^24 in magnitude are resolved; a row
  * with larger ones, which binary32 no longer tells apart, may come out as NaN.
  * Errors: TBQ4_ERR_NULL, TBQ4_ERR_ALIGN, TBQ4_ERR_SHAPE, TBQ4_ERR_CAPACITY,

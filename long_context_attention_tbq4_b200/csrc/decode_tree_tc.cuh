@@ -21,8 +21,12 @@
 //         to shared memory as it lies, token by token, and enters as the
 //         MN-major operand (no transposition anywhere).
 //   Q     q_rot times a power of two that brings the block's largest finite
-//         channel below 2^15: 28 binades of rows below the largest keep all
-//         11 bits.  kTerms = 2 adds the remainder as a second fp16 term.
+//         channel below 2^15.  kTerms = 2 adds the remainder as a second fp16
+//         term.  Where a row's largest channel lies more than 2^14 below the
+//         block's (a row may hold anything in a padded tree), each row takes a
+//         power of two of its own, and the softmax puts it back into S: a row's
+//         channels are rounded by 2^-25 of its own largest at worst, 2^-11 (or
+//         2^-22) relative above that.
 //   P'    p m 2^8 <= 2^15 (p <= 2^6), thread = token writes eight rows per
 //         16-byte store (MN-major).  The scale's power of two lies in V's
 //         levels, so what a weight is rounded to depends on its own row and
@@ -99,9 +103,10 @@ constexpr int kOffNegM = kOffSig + 2 * kSig * kTileT * 4;  // minus the running 
 constexpr int kOffXch = kOffNegM + 128 * 4;             // [4][128] floats
 constexpr int kOffLinv = kOffXch + 4 * 128 * 4;         // [128] floats
 constexpr int kOffFactor = kOffLinv;                    // [128] floats, before those
-constexpr int kOffVis = kOffLinv + 128 * 4;             // [64 nodes][4] words: rows that see it
+constexpr int kOffRow = kOffLinv + 128 * 4;             // [128]: a row's largest |q_rot|, then its power of two
+constexpr int kOffVis = kOffRow + 128 * 4;              // [64 nodes][4] words: rows that see it
 constexpr int kOffSegment = kOffVis + kMaxNodes * 16;   // the first Segment, the CTA's units
-constexpr int kOffQMax = kOffSegment + 56;                // bits of the largest |q_rot|
+constexpr int kOffQMax = kOffSegment + 56;              // bits of the largest |q_rot|, of the least row's
 constexpr int kOffTmem = kOffQMax + 8;
 constexpr int kOffBars = kOffTmem + 8;
 constexpr int kTreeBars = 2 * kRaw + 10 + 1;
@@ -228,7 +233,29 @@ struct Soft {
     int t, lane, wg;                        // token of the tile, lane, warpgroup
     uint32_t weight;                        // what its arrival counts (kPArrivals)
     float c2;                               // log2 logit = S S_k c2
+    bool spread;                            // S is yet to be multiplied by its rows' powers of two
 };
+
+// S of a tile by its rows' powers of two, in place.
+template <int kN>
+__device__ __forceinline__ void spread_rows(const Soft &c, int it, bool &ok) {
+    const int b = it & 1;
+    wait_or_fail(ok, c.bx + 8 * (2 + b), (it >> 1) & 1);
+    tc::fence_after_sync();
+#pragma unroll 1
+    for (int i = 0; i < kN; ++i) {
+        const uint32_t col = c.tmem + ((uint32_t)(c.t & ~31) << 16) + kColS + 128 * b + 32 * c.wg + 8 * i;
+        uint32_t r[8];
+        tc::tmem_ld8(col, r);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            r[k] = __float_as_uint(__uint_as_float(r[k]) *
+                                   ldsf(c.sbase + kOffRow + 128 * c.wg + 32 * i + 4 * k));
+        tc::tmem_st8(col, r);
+    }
+    tc::tmem_wait_st();
+}
 
 // One tile for kN chunks of 8 rows (rows 32 wg + 8 i ..).  The weights are
 // taken with the running maxima as they are, stored, and only then does the
@@ -406,20 +433,24 @@ __device__ __forceinline__ void soft_tile(const Soft &c, int it, bool first, int
 
 // The tiles of a segment, and each row's sum into xch[quarter][row].  A
 // loop for the tiles that every row sees in full and one for the last one or
-// two, so that the frequent one is short straight code.
+// two, so that the frequent one is short straight code.  Rows with powers of
+// two of their own are rare and take the second throughout.  (A test in every
+// tile took 4 % at 5 nodes, products in both loops 3 %: registers.)
 template <int kTerms, int kN>
 __device__ __forceinline__ void soft_segment(const Soft &c, int it, int tiles, int t0, int ctx,
                                              int n_nodes, bool &ok) {
     float lp[8 * kN];
 #pragma unroll
     for (int k = 0; k < 8 * kN; ++k) lp[k] = 0.f;
-    const int full = min(tiles, max(0, (ctx - t0) / kTileT));
+    const int full = c.spread ? 0 : min(tiles, max(0, (ctx - t0) / kTileT));
     int j = 0;
 #pragma unroll 1
     for (; j < full; ++j) soft_tile<kTerms, kN, false>(c, it + j, j == 0, 0, 0, lp, ok);
 #pragma unroll 1
-    for (; j < tiles; ++j)
+    for (; j < tiles; ++j) {
+        if (c.spread) spread_rows<kN>(c, it + j, ok);
         soft_tile<kTerms, kN, true>(c, it + j, j == 0, t0 + j * kTileT + c.t - ctx, n_nodes, lp, ok);
+    }
     float v[32];
 #pragma unroll
     for (int k = 0; k < 32; ++k) v[k] = k < 8 * kN ? lp[k < 8 * kN ? k : 0] : 0.f;
@@ -455,6 +486,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
     float *negm = reinterpret_cast<float *>(smem + kOffNegM);
     float *xch = reinterpret_cast<float *>(smem + kOffXch);
     float *linv = reinterpret_cast<float *>(smem + kOffLinv);
+    float *row_pow2 = reinterpret_cast<float *>(smem + kOffRow);
     uint32_t *vis = reinterpret_cast<uint32_t *>(smem + kOffVis);
     uint32_t *qmax = reinterpret_cast<uint32_t *>(smem + kOffQMax);
 
@@ -474,7 +506,8 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
             mbar_init(pv_done(b), 1);
         }
         mbar_init(drained, 1);
-        *qmax = 0u;
+        qmax[0] = 0u;
+        qmax[1] = 0x7F800000u;
         fence_barrier_init();
     }
     if (warp == 1) {
@@ -785,7 +818,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
             // that runs once per segment costs its instruction fetches.)
             float *stage = reinterpret_cast<float *>(smem + kOffP);   // [rows][128], no P' in it yet
             const int j = lane & 7;
-            float mx = 0.f;
+            float mx = 0.f, mn = INFINITY;
 #pragma unroll 1
             for (int r = 4 * ws + (lane >> 3); r - (lane >> 3) < s.rows; r += 4 * kSoftWarps) {
                 const int c = s.row0 + min(r, s.rows - 1);
@@ -828,31 +861,50 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
                     if (!(k & 2)) butterfly(v[k], v[k + 2]);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) butterfly(v[k], v[k + 4]);
+                float of_row = 0.f;                     // its largest finite channel
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     float4 y;
                     unpack2(mul2(v[2 * k], pack2(rot_c(), rot_c())), y.x, y.y);
                     unpack2(mul2(v[2 * k + 1], pack2(rot_c(), rot_c())), y.z, y.w);
                     const float top = fmaxf(fmaxf(fabsf(y.x), fabsf(y.y)), fmaxf(fabsf(y.z), fabsf(y.w)));
-                    if (isfinite(y.x) && isfinite(y.y) && isfinite(y.z) && isfinite(y.w)) mx = fmaxf(mx, top);
+                    if (isfinite(y.x) && isfinite(y.y) && isfinite(y.z) && isfinite(y.w)) of_row = fmaxf(of_row, top);
                     if (r < s.rows) *reinterpret_cast<float4 *>(stage + r * kD + 4 * j + 32 * k) = y;
                 }
+#pragma unroll
+                for (int m = 1; m < 8; m <<= 1) of_row = fmaxf(of_row, __shfl_xor_sync(kFull, of_row, m));
+                if (j == 0 && r < s.rows) row_pow2[r] = of_row;
+                mx = fmaxf(mx, of_row);
+                if (of_row > 0.f) mn = fminf(mn, of_row);
             }
             mx = warp_max(mx);
-            if (lane == 0 && mx > 0.f) atomicMax(qmax, __float_as_uint(mx));
+            mn = -warp_max(-mn);
+            if (lane == 0 && mx > 0.f) {
+                atomicMax(qmax, __float_as_uint(mx));
+                atomicMin(qmax + 1, __float_as_uint(mn));
+            }
             for (int r = ws * 32 + lane; r < kRows; r += 32 * kSoftWarps) negm[r] = -kLowest;
             soft_sync();
-            const float big = __uint_as_float(*qmax);
-            int e2 = 0;
-            if (big > 0.f) frexpf(big, &e2);            // big < 2^e2
-            e2 = max(e2, -100);
-            const float up = ldexpf(1.0f, 15 - e2);
+            // x < 2^exponent(x); 2^(15 - exponent(x)) brings it below 2^15
+            auto exponent = [](float x) { return max((int)(__float_as_uint(x) >> 23) - 126, -100); };
+            auto pow2 = [](int e) { return __uint_as_float((uint32_t)(127 + e) << 23); };
+            const float big = __uint_as_float(qmax[0]);
+            const bool spread = __uint_as_float(qmax[1]) < big * 0x1p-14f;
+            const int e2 = exponent(big);
             // log2 logit = S skc with skc = S_k c (levels are (2n - 15) 2^-11)
-            const float c2 = p.scale * (1.4426950408889634f * 2048.0f / 15.0f) * ldexpf(1.0f, e2 - 15);
+            const float c2 = p.scale * (1.4426950408889634f * 2048.0f / 15.0f) *
+                             (spread ? 1.0f : pow2(e2 - 15));
             // 16 lanes per row, eight dimensions each
 #pragma unroll 1
             for (int r = 2 * ws + (lane >> 4); r < N; r += 2 * kSoftWarps) {
                 const int ch = lane & 15;
+                int er = e2;
+                if (spread) {
+                    if (r < s.rows) er = exponent(row_pow2[r]);
+                    __syncwarp();                       // both rows' lanes have read
+                    if (ch == 0) row_pow2[r] = pow2(er - 15);
+                }
+                const float up = pow2(15 - er);
                 float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
                 if (r < s.rows) {
                     a = *reinterpret_cast<const float4 *>(stage + r * kD + 8 * ch);
@@ -877,9 +929,12 @@ tree_tc_kernel(const __grid_constant__ TreeParams p) {
             }
             fence_proxy_async();                        // read by the tensor core
             ready_sync();
-            if (ws == 0 && lane == 0) *qmax = 0u;       // for the next segment (read before the barrier)
+            if (ws == 0 && lane == 0) {                 // for the next segment (read before the barrier)
+                qmax[0] = 0u;
+                qmax[1] = 0x7F800000u;
+            }
 
-            const Soft sc = {sbase, tmem, bx, t, lane, wg, kPArrivals / 4 / ((nch + 3) >> 2), c2};
+            const Soft sc = {sbase, tmem, bx, t, lane, wg, kPArrivals / 4 / ((nch + 3) >> 2), c2, spread};
             const int t0 = s.tile0 * kTileT;
             const int mine = min(4, nch - 4 * wg);      // chunks of this warpgroup
             if (mine == 4)

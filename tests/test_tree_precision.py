@@ -78,3 +78,27 @@ def test_many_small_weights_beside_a_large_one(T):  # noqa: F811
     want, eps, amp = tree_attention(q, s["kc"], s["vc"], s["ctx"], s["n"], s["mask"], 128 ** -0.5, 5, table)
     assert T.tbq4_get_device_status() == 0
     check_tree(got, want.expand(B, 1, 1, 128), eps.expand(B, 1, 1), amp.expand(B, 1, 1, 1))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("out", ["float16", "bfloat16"])
+@pytest.mark.parametrize("size", [1e6, 1e12, 1e30])
+def test_a_huge_query_changes_no_other_row(T, out, size):  # noqa: F811
+    # finite, as memory that nobody wrote may hold in the rows of a padded tree;
+    # the row itself is beyond what logits resolve, and its neighbours are not
+    import torch
+    from tree_helpers import check_tree, tree_attention
+    for dtype in ("float32", "bfloat16"):
+        s = make(T, 84, 1, 12, 2, 4, [300], dtype=dtype, out=out)
+        want = tree_attention(s["q"], s["kc"], s["vc"], s["ctx"], s["n"], s["mask"], 128 ** -0.5, 5)
+        s["q"][0, 2, 1] *= size
+        s["q"][0, 5, 6] *= 1e-30                        # and a tiny one: the plain mean of what it sees
+        tiny = s["q"].clone()
+        tiny[0, 2, 1] = 0
+        small = tree_attention(tiny, s["kc"], s["vc"], s["ctx"], s["n"], s["mask"], 128 ** -0.5, 5)
+        got = call(T, s)
+        ok = torch.ones(s["q"].shape[:3], dtype=torch.bool, device="cuda")
+        ok[0, 2, 1] = ok[0, 5, 6] = False
+        check_tree(got[ok], *(x[ok] for x in want))
+        check_tree(got[0, 5, 6][None], *(x[0, 5, 6][None] for x in small))
+        assert T.tbq4_get_device_status() == 0
