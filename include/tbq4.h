@@ -462,7 +462,8 @@ TBQ4_API tbq4_status tbq4_rope_append_paged(
  * Constraints: 1 <= B <= 1024, 1 <= T <= 64, Hq % Hkv == 0, Hq / Hkv <= 8.
  * Precision: products of the cache's exact levels, sums and softmax
  * statistics in binary32; queries and softmax weights enter the tensor cores
- * as fp16 (TBQ4_BF16 outputs) or as pairs of fp16 terms (TBQ4_F16 outputs).
+ * as fp16 where queries and outputs are both TBQ4_BF16, else as pairs of fp16
+ * terms (TBQ4_F32 or TBQ4_F16 queries with a TBQ4_BF16 output ask for those).
  * One term's rounding is 2^-11 relative, a pair's 2^-22; below that a weight is
  * held to 2^-29 of its row's largest weight, a pair to 2^-40, or finer (for V
  * scales S below 2^-14, 2^-14 / S times that).

@@ -566,7 +566,9 @@ def tbq4_attn_tree(q, k_cache, v_cache, ctx_lens, tree_mask, softmax_scale, sign
     (default: T everywhere) int32 [B]; tree_mask int64 [B][T] or [T] (one tree
     for all): bit j of entry i set where node i sees node j.  Returns
     [B][T][Hq][128] in out's dtype (default: bfloat16 for bfloat16 queries,
-    else float16); rows of nodes >= n_nodes[b] are not written."""
+    else float16); rows of nodes >= n_nodes[b] are not written.  bfloat16
+    queries with a bfloat16 out are computed in 11 bits (a term per operand),
+    every other pair in 22, in up to twice the time."""
     index, (B, Hkv, cap, _) = _cache_pair(k_cache, v_cache, ("k_cache", "v_cache"))
     return _attn_tree("tbq4_attn_tree", q, k_cache, v_cache, Hkv, B, (cap,), (), index, ctx_lens,
                       tree_mask, softmax_scale, sign_seed, n_nodes, workspace, out, out_dtype, stream)

@@ -39,9 +39,14 @@
 //         own: 2^-22 relative, or 2^-40 of the row's largest weight.  (Added to
 //         O itself, the remainder is subnormal where P' < 2^-3: 32,767 tokens
 //         20 below a token without V, which make the row, were 6 % off.)
-// One term rounds a query or a weight by up to 2^-11 relative, a tenth of a
-// bf16 output's own rounding; fp16 outputs, which that would double, take two
-// terms (22 bits) and blocks of 64 rows in the same shared memory.
+// One term rounds a query or a weight by up to 2^-11 relative: an eighth of what
+// a bf16 query and a bf16 output are rounded by themselves.  It is taken where
+// both are bf16 (rel-L2 against 64 bits 1.69e-3 to 1.79e-3 where an fp32
+// computation rounded to bf16 has 1.64e-3 to 1.67e-3, most of it the queries').
+// Everything else takes two terms (22 bits), in blocks of 64 rows in the same
+// shared memory: sharp rows of fp32 queries lose more to an 11-bit query than to
+// a bf16 output.  Two terms throughout, bf16 at 262K in a graph: 5 nodes 76 us
+// instead of 68, 16 nodes 156 instead of 84, 64 nodes 434 instead of 242.
 //
 // Softmax.  thread = token, so its S_k and S_v are scalars and a row's
 // running maximum is one number for all threads (shared memory).  The

@@ -798,9 +798,12 @@ tbq4_status rope_impl(const Rows &q, const Rows &k, const Rows &v, int dtype, in
     return launch_status();
 }
 
-// Rows per block of tree attention: fp16 outputs take two terms per operand
-// and half the rows (see tree_tc_kernel).
-int tree_rows(int out_dtype) { return out_dtype == TBQ4_F16 ? 64 : 128; }
+// Terms per operand of tree attention, and rows per block (two terms fill the
+// same shared memory with half the rows; see decode_tree_tc.cuh).
+int tree_terms(int q_dtype, int out_dtype) {
+    return q_dtype == TBQ4_BF16 && out_dtype == TBQ4_BF16 ? 1 : 2;
+}
+int tree_rows(int terms) { return 128 / terms; }
 
 size_t tree_ws_bytes(int rows) {
     return align_up((size_t)2 * kNumSMs * rows * (kD * sizeof(float) + sizeof(float2)), kWsAlign);
@@ -826,7 +829,7 @@ tbq4_status tree_impl(const void *q, int q_dtype, const uint8_t *k, const uint8_
         !std::isfinite(softmax_scale))
         return TBQ4_ERR_SHAPE;
     if (capacity <= 0 || capacity % 8 != 0 || capacity > INT32_MAX - 256) return TBQ4_ERR_CAPACITY;
-    const int rows = tree_rows(out_dtype);
+    const int terms = tree_terms(q_dtype, out_dtype), rows = tree_rows(terms);
     // units (tiles of all works) are numbered in 32 bits
     const int64_t most = ceil_div(capacity, tree::kTileT) * ceil_div((int64_t)T * (Hq / Hkv), rows) *
                          Hkv;
@@ -874,7 +877,7 @@ tbq4_status tree_impl(const void *q, int q_dtype, const uint8_t *k, const uint8_
     p.out_type = out_dtype;
     p.out_elems = elems;
     static bool attr1[64] = {}, attr2[64] = {};
-    const bool two = out_dtype == TBQ4_F16;
+    const bool two = terms == 2;
     const void *fn = two ? (const void *)tree::tree_tc_kernel<2> : (const void *)tree::tree_tc_kernel<1>;
     if (!ensure_smem_attr(fn, tree::kTcSmem, two ? attr2 : attr1)) return TBQ4_ERR_LAUNCH;
     // the kernel moves registers between its warpgroups (setmaxnreg), which
@@ -1012,7 +1015,7 @@ size_t tbq4_tree_workspace_bytes(int B, int T, int Hq, int Hkv) {
     if (B <= 0 || B > tree::kMaxBatch || T <= 0 || T > tree::kMaxNodes || Hkv <= 0 || Hq <= 0 ||
         Hq % Hkv != 0 || Hq / Hkv > kMaxGroup)
         return 0;
-    return tree_ws_bytes(tree_rows(TBQ4_BF16));
+    return tree_ws_bytes(tree_rows(1));
 }
 
 tbq4_status tbq4_attn_tree(const void *q, int q_dtype, const uint8_t *k_cache,

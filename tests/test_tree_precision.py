@@ -102,3 +102,26 @@ def test_a_huge_query_changes_no_other_row(T, out, size):  # noqa: F811
         check_tree(got[ok], *(x[ok] for x in want))
         check_tree(got[0, 5, 6][None], *(x[0, 5, 6][None] for x in small))
         assert T.tbq4_get_device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["float32", "float16"])
+@pytest.mark.parametrize("page", [0, 64])
+def test_sharp_queries_of_more_than_bf16_bits(T, dtype, page):  # noqa: F811
+    """Logits of some +-100 over 20,000 tokens, bf16 output.  Queries that carry
+    more bits than bf16 go in as pairs: a logit is off by 2^-22 of the sum of
+    |q_d k_d| (eps is 2^-11 of it), a weight by 2^-22 and by what that does to
+    it, sums and exponentials by 2^-18; and the output is rounded once, by at
+    most 2^-8 relative, uniformly, so that the 2-norm is within 2^-8 / sqrt(3)
+    but for chance (9,216 elements: a few percent)."""
+    import torch
+    from tree_helpers import tree_attention
+    s = make(T, 85, 1, 12, 2, 3, [20000], dtype=dtype, out="bfloat16", gain=30.0, page=page)
+    got = call(T, s, fill=3.5).double()
+    assert T.tbq4_get_device_status() == 0
+    want, eps, amp = tree_attention(s["q"], s["kc"], s["vc"], s["ctx"], s["n"], s["mask"], 128 ** -0.5, 5, s["table"])
+    x = torch.expm1(eps * 2.0 ** -11)[..., None] * (1 + 2.0 ** -22) + 2.0 ** -22 + 2.0 ** -18
+    err = (got - want).abs()
+    assert bool((err <= 2 * x * amp + 2.0 ** -8 * (want.abs() + 2 * x * amp)).all())
+    rest = float((2 * x * amp).expand_as(want).norm() / want.norm())
+    assert float(err.norm() / want.norm()) <= 1.05 * 2.0 ** -8 / 3 ** 0.5 + rest, (float(err.norm() / want.norm()), rest)
