@@ -385,7 +385,8 @@ typedef enum { TBQ4_F32 = 0, TBQ4_F16 = 1, TBQ4_BF16 = 2 } tbq4_dtype;
  *   caches    the rotated keys and the values, encoded as by
  *             tbq4_quantize_append (from binary32: a key is not rounded to
  *             the input's type between rotation and encoding).  Bytes are
- *             defined bit for bit.
+ *             defined bit for bit, for rows of finite values: a row with a
+ *             NaN or an infinity gets a block, but which is not defined.
  *   q_out     the rotated queries, rounded once (to nearest even) to the
  *             input's type.
  * Arguments:

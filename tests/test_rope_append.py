@@ -270,3 +270,53 @@ def test_equals_separate_quantize_append(T):
     T.tbq4_quantize_append(k[None], start, a[2], 9)
     T.tbq4_quantize_append(v[None], start, a[3], 9)
     assert torch.equal(a[0], a[2]) and torch.equal(a[1], a[3])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rot,interleaved", [(0, False), (128, False), (64, True), (96, False)])
+def test_every_scale_of_rows(T, rot, interleaved):
+    # rows of zeros, of scales that round to 0 or are subnormal in fp16, that
+    # saturate at 65504 or fall just short of it: the encoder's rare branch
+    import torch
+    n, Hkv = 240, 3
+    gen = torch.Generator("cuda").manual_seed(rot + interleaved)
+    x = torch.randn((n, 2 * Hkv, 128), generator=gen, device="cuda")
+    size = torch.tensor([0.0, 1e-9, 2e-8, 3e-8, 1e-7, 1e-6, 2e-5, 1.0, 2e4, 3e4, 1e6, 1e30], device="cuda")
+    x *= size[torch.arange(n, device="cuda") % 12][:, None, None]
+    x[5, 0] = 0.0
+    x[5, 0, 7] = 65504.0                                # spread evenly: 65504 / sqrt(128) everywhere
+    pos = np.arange(n) * 11
+    freq = _frequencies(rot, 1e5)
+    kc, vc = (torch.full((1, Hkv, n, 66), 0xA5, dtype=torch.uint8, device="cuda") for _ in "kv")
+    T.tbq4_rope_append(x[:, :Hkv], x[:, Hkv:], torch.arange(n, dtype=torch.int32, device="cuda"),
+                       torch.from_numpy(freq).cuda() if rot else None, kc, vc,
+                       positions=torch.from_numpy(pos).to(torch.int32).cuda(), interleaved=interleaved, sign_seed=SEED)
+    assert T.tbq4_get_device_status() == 0
+    rows = x.cpu().numpy()
+    for got, r in ((kc, rope(rows[:, :Hkv], pos, freq[: rot // 2], interleaved)), (vc, rows[:, Hkv:])):
+        got = got[0].cpu().numpy().transpose(1, 0, 2)
+        scales = got[..., :2].copy().view(np.uint16)
+        assert (scales == 0).any() and ((scales > 0) & (scales < 0x400)).any() and (scales == 0x7BFF).any()
+        np.testing.assert_array_equal(got, encoded(r, SEED))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq", [1, 4, 7])
+@pytest.mark.parametrize("rot,interleaved", [(128, False), (128, True), (64, False), (64, True), (96, False), (0, False)])
+@pytest.mark.parametrize("n", [1, 9, 6000])
+def test_in_place_queries(T, n, rot, interleaved, Hq):
+    # a pair's halves are read again from the row that is written over: with one
+    # row to a half-warp, an odd count, and as many warps to a token as it has
+    # pairs of rows, or one
+    import torch
+    g = torch.Generator("cuda").manual_seed(n + rot + Hq)
+    for dtype in (torch.float32, torch.bfloat16):
+        q = torch.randn((n, Hq, 128), generator=g, device="cuda").to(dtype)
+        k, v = (torch.randn((n, 1, 128), generator=g, device="cuda").to(dtype) for _ in "kv")
+        slots = torch.arange(n, dtype=torch.int32, device="cuda")
+        inv = torch.from_numpy(_frequencies(rot)).cuda() if rot else None
+        caches = [torch.zeros((1, 1, (n + 7) // 8 * 8, 66), dtype=torch.uint8, device="cuda") for _ in range(4)]
+        want = T.tbq4_rope_append(k, v, slots, inv, *caches[:2], q=q, interleaved=interleaved)
+        got = T.tbq4_rope_append(k, v, slots, inv, *caches[2:], q=q, q_out=q, interleaved=interleaved)
+        assert got.data_ptr() == q.data_ptr() and torch.equal(got, want)
+        assert torch.equal(caches[0], caches[2]) and torch.equal(caches[1], caches[3])

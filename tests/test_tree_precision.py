@@ -125,3 +125,35 @@ def test_sharp_queries_of_more_than_bf16_bits(T, dtype, page):  # noqa: F811
     assert bool((err <= 2 * x * amp + 2.0 ** -8 * (want.abs() + 2 * x * amp)).all())
     rest = float((2 * x * amp).expand_as(want).norm() / want.norm())
     assert float(err.norm() / want.norm()) <= 1.05 * 2.0 ** -8 / 3 ** 0.5 + rest, (float(err.norm() / want.norm()), rest)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,out", [("bfloat16", "bfloat16"), ("float32", "bfloat16"), ("float16", "float16")])
+@pytest.mark.parametrize("gain", [1.0, 6.0])
+def test_error_of_ordinary_calls(T, dtype, out, gain):  # noqa: F811
+    """The 2-norm of the error, from independent roundings.  A rounding by at most
+    h is uniform, so its rms is h / sqrt(3).  The output's h is 2^-8 (bf16) or
+    2^-11 relative; a query channel's and a weight's h 2^-11 relative for one
+    term, 2^-22 for pairs, and 2^-18 for sums and exponentials.  A channel's
+    moves logit t by scale q_d k_td of it; a weight off by x_t moves the row by
+    p_t x_t (v_t - o).  Those add up in squares, with 10 % left for chance."""
+    import torch
+    from tree_helpers import dequantised, rotation, tree_attention
+    s = make(T, 86, 1, 12, 2, 3, [3000], dtype=dtype, out=out, gain=gain)
+    got = call(T, s, fill=3.5).double()
+    want, _, _ = tree_attention(s["q"], s["kc"], s["vc"], s["ctx"], s["n"], s["mask"], 128 ** -0.5, 5)
+    h = 2.0 ** -11 if dtype == out == "bfloat16" else 2.0 ** -22
+    R, total = rotation(5, "cuda"), (torch.finfo(s["out"]).eps / 2) ** 2 / 3 * float(want.norm()) ** 2
+    sees = torch.ones((12, 3012), dtype=torch.bool, device="cuda")
+    sees[:, 3000:] = (s["mask"][0][:, None] >> torch.arange(12, device="cuda")) & 1 == 1
+    for head in range(6):
+        k, v = (dequantised(s[c][0, head // 3, :3012]) for c in ("kc", "vc"))
+        q = s["q"][0, :, head].double() @ R.T
+        p = ((q @ k.T) / 128 ** 0.5).masked_fill(~sees, float("-inf")).softmax(-1)
+        x2 = (q ** 2) @ (k ** 2).T / 128 * h ** 2 / 3 + h ** 2 / 3 + 2.0 ** -36
+        o = p @ v
+        dist = (v ** 2).sum(-1)[None] - 2 * o @ v.T + (o ** 2).sum(-1, keepdim=True)
+        total += float((p ** 2 * x2 * dist).sum())
+    err = float((got - want).norm())
+    print(f"error {err / float(want.norm()):.3e}, expected at most {(total ** 0.5) / float(want.norm()):.3e}")
+    assert err <= 1.1 * total ** 0.5
