@@ -348,7 +348,8 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
 
 def _check(name, t, dtype, ndim, index):
     """A contiguous CUDA tensor of this type and rank on device `index`."""
-    if not (t.dtype is dtype and t.dim() == ndim and t.is_contiguous() and t.get_device() == index):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == ndim and t.is_contiguous()
+            and t.get_device() == index):
         _need(t, dtype, name, ndim)
         raise ValueError(f"{name} lies on {t.device}, other tensors on cuda:{index}")
 
@@ -405,8 +406,8 @@ def _rows(name, t, dtype, index, tokens, heads):
 
 def _rope_append(name, k, v, slots, inv_freq, kc, vc, Hkv, B, layout, index, q, positions, seq_ids,
                  interleaved, sign_seed, q_out, stream):
-    for t, what in ((k, "k"), (v, "v"), (q, "q")):
-        if t is not None and (not isinstance(t, torch.Tensor) or t.dtype not in _DTYPES or t.dim() != 3):
+    for t, what in ((k, "k"), (v, "v"), (k if q is None else q, "q")):
+        if not isinstance(t, torch.Tensor) or t.dtype not in _DTYPES or t.dim() != 3:
             raise TypeError(f"{what} must be a [tokens][heads][128] CUDA tensor of float32, float16 or "
                             f"bfloat16")
     dtype, n = k.dtype, k.shape[0]
@@ -526,7 +527,7 @@ def _attn_tree(name, q, kc, vc, Hkv, B, cap, paged, index, ctx_lens, mask, softm
     _check("ctx_lens", ctx_lens, torch.int32, 1, index)
     if d != D or Bq != B or ctx_lens.shape[0] != B:
         raise ValueError("shape mismatch between q, caches and ctx_lens")
-    _check("tree_mask", mask, torch.int64, mask.dim(), index)
+    _check("tree_mask", mask, torch.int64, getattr(mask, "ndim", None), index)
     per = mask.numel() // T if T else 0
     if mask.shape[-1:] != (T,) or (mask.dim() == 2 and per != B) or not 1 <= mask.dim() <= 2:
         raise ValueError(f"tree_mask must be [{T}] or [{B}][{T}], got {tuple(mask.shape)}")
@@ -538,12 +539,16 @@ def _attn_tree(name, q, kc, vc, Hkv, B, cap, paged, index, ctx_lens, mask, softm
         nodes = n_nodes.data_ptr()
     if workspace is None:
         workspace = _empty(q, (max(lib.tbq4_tree_workspace_bytes(B, T, Hq, Hkv), 1),), torch.uint8, stream)
+    elif not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace must be a CUDA tensor")
     elif not workspace.is_contiguous() or workspace.get_device() != index:
         raise ValueError(f"workspace must be contiguous, on cuda:{index}")
     if out is None:
         if out_dtype is None:
             out_dtype = torch.bfloat16 if q.dtype is torch.bfloat16 else torch.float16
         out = _empty(q, shape, out_dtype, stream)
+    elif not isinstance(out, torch.Tensor):
+        raise TypeError("out must be a CUDA tensor")
     elif out_dtype is not None and out.dtype is not out_dtype:
         raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
     if out.dtype not in (torch.float16, torch.bfloat16):
