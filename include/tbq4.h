@@ -406,15 +406,15 @@ typedef enum { TBQ4_F32 = 0, TBQ4_F16 = 1, TBQ4_BF16 = 2 } tbq4_dtype;
  *   rot_dim    0 .. 128, a multiple of 8
  *   k_cache,
  *   v_cache    as tbq4_quantize_append (or pools and a block table, as
- *              tbq4_quantize_append_paged); distinct
+ *              tbq4_quantize_append_paged), not over one another
  *   q_out      device, [n_tokens][Hq][128] of type `dtype`, 16-byte aligned;
  *              may be q itself where q has those strides, and lies over
- *              nothing else of q, k and v
+ *              nothing else of q, k, v and the caches
  * A token whose id is >= B, or whose slot or page lies outside the cache, has
  * no row written into the caches and flags TBQ4_ERR_CAPACITY in the device
  * status.
  * Errors: TBQ4_ERR_NULL, TBQ4_ERR_ALIGN (pointers, strides), TBQ4_ERR_SHAPE
- * (dtype, sizes, rot_dim, k_cache == v_cache, q_out over q, k or v),
+ * (dtype, sizes, rot_dim, caches that overlap, q_out over one or over q, k or v),
  * TBQ4_ERR_CAPACITY (capacity), TBQ4_ERR_LAUNCH.
  */
 TBQ4_API tbq4_status tbq4_rope_append(const void *q, int64_t q_token_stride, int64_t q_head_stride,
@@ -503,19 +503,19 @@ TBQ4_API tbq4_status tbq4_attn_tree_paged(const void *q, int q_dtype, const uint
  * new_lens[b] on are left as they are.
  *   k_caches,
  *   v_caches  host arrays of n_layers device pointers, each cache (or pool) as
- *             tbq4_attn_decode's and all distinct; they are read during the
- *             call only
- *             call only.  Pages that hold ctx_lens[b] or a later slot belong to
- *             one sequence each (a context may share full pages before them).
+ *             tbq4_attn_decode's, none over another; the arrays are read during
+ *             the call only.  Pages that hold ctx_lens[b] or a later slot belong
+ *             to one sequence each (a context may share full pages before them).
  *   path      device, int32 [B][max_path], 1 <= max_path <= 64
  *   n_accept  device, int32 [B], each 0 .. max_path
- *   new_lens  device, int32 [B], or NULL; not over ctx_lens, n_accept or path
+ *   new_lens  device, int32 [B], or NULL; not over ctx_lens, n_accept, path or
+ *             a cache
  * A count outside 0 .. max_path, or a context that leaves no room for it,
  * moves nothing of that sequence (its new length is its old one); a node whose
  * slot or page lies outside the cache is skipped.  Both flag
  * TBQ4_ERR_CAPACITY in the device status.
- * Errors: TBQ4_ERR_NULL, TBQ4_ERR_ALIGN, TBQ4_ERR_SHAPE (sizes, a cache given
- * twice, new_lens over an input), TBQ4_ERR_CAPACITY, TBQ4_ERR_LAUNCH.
+ * Errors: TBQ4_ERR_NULL, TBQ4_ERR_ALIGN, TBQ4_ERR_SHAPE (sizes, caches that
+ * overlap, new_lens over one or an input), TBQ4_ERR_CAPACITY, TBQ4_ERR_LAUNCH.
  */
 TBQ4_API tbq4_status tbq4_tree_accept(uint8_t *const *k_caches, uint8_t *const *v_caches,
                                       int n_layers, const int32_t *ctx_lens, const int32_t *path,

@@ -735,6 +735,9 @@ tbq4_status rope_impl(const Rows &q, const Rows &k, const Rows &v, int dtype, in
         return TBQ4_ERR_SHAPE;
     if (capacity <= 0 || capacity % 8 != 0) return TBQ4_ERR_CAPACITY;
     if (n_tokens == 0) return TBQ4_OK;
+    const int64_t cache_bytes =
+        (pg ? pg->n_pages * pg->page_size : (int64_t)B * capacity) * Hkv * kBlockBytes;
+    if (overlap(kc, cache_bytes, vc, cache_bytes)) return TBQ4_ERR_SHAPE;
     if (Hq > 0) {
         // warps write queries while others still read rows: nothing that they
         // read may lie there, but for a row of q in its own place
@@ -743,7 +746,8 @@ tbq4_status rope_impl(const Rows &q, const Rows &k, const Rows &v, int dtype, in
                               (Hq == 1 || q.head == kD);
         if ((!in_place && overlap(q.p, q.extent(n_tokens, Hq, dtype), q_out, out_bytes)) ||
             overlap(k.p, k.extent(n_tokens, Hkv, dtype), q_out, out_bytes) ||
-            overlap(v.p, v.extent(n_tokens, Hkv, dtype), q_out, out_bytes))
+            overlap(v.p, v.extent(n_tokens, Hkv, dtype), q_out, out_bytes) ||
+            overlap(kc, cache_bytes, q_out, out_bytes) || overlap(vc, cache_bytes, q_out, out_bytes))
             return TBQ4_ERR_SHAPE;
     }
     RopeParams p = {};
@@ -776,7 +780,7 @@ tbq4_status rope_impl(const Rows &q, const Rows &k, const Rows &v, int dtype, in
         p.pm.page_size = pg->page_size;
         p.pm.n_pages = pg->n_pages;
     }
-    p.pm.cache_bytes = (pg ? pg->n_pages * pg->page_size : (int64_t)B * capacity) * Hkv * kBlockBytes;
+    p.pm.cache_bytes = cache_bytes;
     p.kc = kc;
     p.vc = vc;
     p.q_out = q_out;
@@ -948,7 +952,12 @@ tbq4_status accept_impl(uint8_t *const *k_caches, uint8_t *const *v_caches, int 
         if (!aligned(all[i], 16)) return TBQ4_ERR_ALIGN;
     }
     std::sort(all, all + 2 * n_layers, std::less<const uint8_t *>());
-    if (std::adjacent_find(all, all + 2 * n_layers) != all + 2 * n_layers) return TBQ4_ERR_SHAPE;
+    const int64_t cache_bytes =
+        (pg ? pg->n_pages * pg->page_size : (int64_t)B * capacity) * Hkv * kBlockBytes;
+    for (int i = 0; i < 2 * n_layers; ++i)
+        if ((i > 0 && overlap(all[i - 1], cache_bytes, all[i], cache_bytes)) ||
+            overlap(all[i], cache_bytes, new_lens, 4 * (int64_t)B))
+            return TBQ4_ERR_SHAPE;
     AcceptParams p = {};
     p.B = B;
     p.Hkv = Hkv;
@@ -957,13 +966,12 @@ tbq4_status accept_impl(uint8_t *const *k_caches, uint8_t *const *v_caches, int 
     p.ctx_lens = ctx_lens;
     p.path = path;
     p.n_accept = n_accept;
-    p.cache_bytes = (int64_t)B * capacity * Hkv * kBlockBytes;
+    p.cache_bytes = cache_bytes;
     if (pg) {
         p.table = pg->block_table;
         p.max_pages = pg->max_pages;
         p.page_size = pg->page_size;
         p.n_pages = pg->n_pages;
-        p.cache_bytes = pg->n_pages * pg->page_size * Hkv * kBlockBytes;
     }
     for (int l0 = 0; l0 < n_layers; l0 += kAcceptLayers) {
         const int n = std::min(kAcceptLayers, n_layers - l0);

@@ -320,3 +320,14 @@ def test_in_place_queries(T, n, rot, interleaved, Hq):
         got = T.tbq4_rope_append(k, v, slots, inv, *caches[2:], q=q, q_out=q, interleaved=interleaved)
         assert got.data_ptr() == q.data_ptr() and torch.equal(got, want)
         assert torch.equal(caches[0], caches[2]) and torch.equal(caches[1], caches[3])
+
+
+@pytest.mark.parametrize("paged", [False, True])
+def test_refuses_caches_that_overlap(paged):
+    far = dict(q=C.c_void_p(0x300000), k=C.c_void_p(0x400000), v=C.c_void_p(0x500000), qo=C.c_void_p(0x600000))
+    size = (8 * 32 if paged else 2 * 64) * 2 * 66
+    assert _call(paged, **{**far, "vc": C.c_void_p(0x10000 + size - 16)}) == 3
+    assert _call(paged, **{**far, "vc": C.c_void_p(0x10000 - size + 16)}) == 3
+    # rotated queries over a cache
+    assert _call(paged, **{**far, "qo": C.c_void_p(0x10000 + size - 16)}) == 3
+    assert _call(paged, **{**far, "qo": C.c_void_p(0x20000 - 16)}) == 3

@@ -121,3 +121,13 @@ def test_bad_counts_and_nodes(T):
     assert status == 4 and new == [6, 6, 6]
     assert torch.equal(k[1, :, 4], base[1, :, 5]) and torch.equal(k[1, :, 5], base[1, :, 5])
     assert torch.equal(k[2, :, 4], base[2, :, 4]) and torch.equal(k[2, :, 5], base[2, :, 7])
+
+
+@pytest.mark.parametrize("paged", [False, True])
+def test_refuses_caches_that_overlap(paged):
+    # one cache's blocks would move while another's are read
+    size = (8 * 32 if paged else 2 * 64) * 2 * 66
+    assert _call(paged, k=[A], v=[A + size - 16]) == 3
+    assert _call(paged, k=[A, 0x80000], v=[A2, 0x80000 + size - 16]) == 3
+    assert _call(paged, k=[A + 4 * size], v=[A + 3 * size + 16]) == 3
+    assert _call(paged, new=A2 + 64) == 3                # the new lengths in a cache
