@@ -70,6 +70,7 @@
 // records the error and goes on without waiting, so the named barriers of
 // its warpgroup and of the CTA always fill.
 #pragma once
+#include "decode_mq.cuh"
 #include "decode_tree.cuh"
 #include "tcgen05.cuh"
 

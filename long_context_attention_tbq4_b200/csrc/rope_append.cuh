@@ -61,12 +61,11 @@ __device__ __forceinline__ void store4(void *p, int type, int64_t idx, const flo
 struct RopeParams {
     const void *q, *k, *v;             // rows of 128, strides in elements
     int64_t q_tok, q_head, k_tok, k_head, v_tok, v_head;
-    int type;                          // ElemType of q, k, v and q_out
     int n_tokens, Hq, Hkv, B;
     int per_seq;                       // seq_ids == nullptr: token i is of sequence i / per_seq
     const int32_t *seq_ids, *slots, *positions;   // positions may be nullptr: the slots
     const double *inv_freq;            // [rot / 2]
-    int rot, interleaved;
+    int rot;
     int64_t capacity;
     uint64_t sign_lo, sign_hi;
     PageMap pm;                        // table == nullptr: contiguous caches

@@ -760,7 +760,6 @@ tbq4_status rope_impl(const Rows &q, const Rows &k, const Rows &v, int dtype, in
     p.k_head = k.head;
     p.v_tok = v.tok;
     p.v_head = v.head;
-    p.type = dtype;
     p.n_tokens = n_tokens;
     p.Hq = Hq;
     p.Hkv = Hkv;
@@ -771,7 +770,6 @@ tbq4_status rope_impl(const Rows &q, const Rows &k, const Rows &v, int dtype, in
     p.positions = positions;
     p.inv_freq = inv_freq;
     p.rot = rot_dim;
-    p.interleaved = interleaved != 0;
     p.capacity = capacity;
     sign_words(sign_seed, &p.sign_lo, &p.sign_hi);
     if (pg) {
