@@ -508,8 +508,7 @@ TBQ4_API tbq4_status tbq4_attn_tree_paged(const void *q, int q_dtype, const uint
  *             to one sequence each (a context may share full pages before them).
  *   path      device, int32 [B][max_path], 1 <= max_path <= 64
  *   n_accept  device, int32 [B], each 0 .. max_path
- *   new_lens  device, int32 [B], or NULL; not over ctx_lens, n_accept, path or
- *             a cache
+ *   new_lens  device, int32 [B], or NULL; not over an input or a cache
  * A count outside 0 .. max_path, or a context that leaves no room for it,
  * moves nothing of that sequence (its new length is its old one); a node whose
  * slot or page lies outside the cache is skipped.  Both flag

@@ -938,6 +938,8 @@ tbq4_status accept_impl(uint8_t *const *k_caches, uint8_t *const *v_caches, int 
         overlap(new_lens, 4 * (int64_t)B, path, 4 * (int64_t)B * max_path))
         return TBQ4_ERR_SHAPE;
     if (capacity <= 0 || capacity % 8 != 0 || capacity > INT32_MAX) return TBQ4_ERR_CAPACITY;
+    if (pg && overlap(new_lens, 4 * (int64_t)B, pg->block_table, 4 * (int64_t)B * pg->max_pages))
+        return TBQ4_ERR_SHAPE;
     const int per = std::min(n_layers, kAcceptLayers);
     if ((int64_t)2 * per * B * Hkv > (int64_t)kAcceptWarps * INT32_MAX) return TBQ4_ERR_SHAPE;
     const uint8_t *all[2 * kMaxAcceptLayers];

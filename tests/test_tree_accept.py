@@ -131,3 +131,5 @@ def test_refuses_caches_that_overlap(paged):
     assert _call(paged, k=[A, 0x80000], v=[A2, 0x80000 + size - 16]) == 3
     assert _call(paged, k=[A + 4 * size], v=[A + 3 * size + 16]) == 3
     assert _call(paged, new=A2 + 64) == 3                # the new lengths in a cache
+    if paged:
+        assert _call(True, new=A + 8) == 3               # or in the block table
