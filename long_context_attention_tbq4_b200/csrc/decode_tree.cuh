@@ -189,10 +189,11 @@ __device__ __forceinline__ void store_out(const TreeParams &p, int b, int g, int
 // A CTA's warps share the work's partials: four warps per row where it has
 // more than kJoinMany, else one, and rows in turn.  A warp takes its partials'
 // maxima and sums first, a lane each, then the rows, kJoinBatch in flight; the
-// warps of a row meet in shared memory.  (Four warps throughout: 8 trees of 25
-// nodes 236 us instead of 224; one throughout: 5 nodes at 262K 83 instead of
-// 79.  A running maximum over partials read one by one cost 10 us more on the
-// long sequences.)
+// warps of a row meet in shared memory.  (kJoinMany 64, so that hardly any row
+// has four: 16 nodes at 262K 87.2 us instead of 83.8, 1 node at 32K 20.0 instead
+// of 18.4; 8: 64 nodes 252.9 instead of 244.3; 4: also 8 trees of 25 nodes 238.6
+// instead of 226.0; 32 is as good as 16.  A running maximum over partials read
+// one by one cost 10 us more on the long sequences.)
 constexpr int kJoinWarps = 16, kJoinMany = 16, kJoinBatch = 8;
 
 __global__ void __launch_bounds__(kJoinWarps * 32)

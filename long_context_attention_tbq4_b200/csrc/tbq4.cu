@@ -676,7 +676,10 @@ tbq4_status tbq4_attn_prefill_chunk(const uint16_t *q, int n_new, int64_t n_cach
 
 namespace {
 
-// Warps per SM that rope-append spreads few tokens over.
+// Warps per SM that rope-append spreads few tokens over: 1,999 tokens of 8/8
+// heads in fp32 take 10.5 us, 11.7 with half as many and 12.0 with twice as many;
+// 200 tokens of 24/4 heads 5.1, 4.8 and 5.1; one token is a warp per pair of rows
+// with any of them.
 constexpr int kRopeFill = 32;
 
 size_t elem_bytes(int dtype) { return dtype == TBQ4_F32 ? 4 : 2; }
@@ -900,8 +903,9 @@ tbq4_status tree_impl(const void *q, int q_dtype, const uint8_t *k, const uint8_
     // the join, a programmatic dependent launch: one CTA per work (or start of
     // a share, when there are more works than shares) and group of rows
     cudaLaunchConfig_t cfg = {};
-    // one CTA per SM, or one per four rows if those are fewer (four per SM: 64
-    // nodes at 262K 248 us instead of 241, 8 trees of 25 nodes 229 instead of 223)
+    // one CTA per SM, or one per four rows if those are fewer (in a graph, with
+    // half as many 16 nodes at 262K take 86.8 us instead of 83.8 and 64 nodes 247.5
+    // instead of 244.3; with twice as many 83.8 and 246.3)
     const int columns = (int)(p.join_starts ? p.n_ctas - 1 : works);
     cfg.gridDim = dim3((unsigned)columns, (unsigned)std::min<int64_t>(ceil_div(std::min(rows, T * p.G), 4),
                                                                       ceil_div(kNumSMs, columns)));
